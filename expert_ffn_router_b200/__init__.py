@@ -24,7 +24,9 @@ HEADER = os.path.join(os.path.dirname(_PKG), "include", "moe.h")
 
 MOE_OK, MOE_EINVAL, MOE_EALIGN, MOE_ENOSPACE, MOE_ECUDA, MOE_ETIMEOUT, MOE_EDEVICE = 0, -1, -2, -3, -4, -5, -6
 MOE_IO_X_HOST, MOE_IO_OUT_HOST = 1, 2  # moe_layer_opts.io_host bits
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_I8 = 0, 1, 2
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
+MOE_GROUP_TOP2, MOE_GROUP_MAX = 0, 1
 MOE_PATH_AUTO, MOE_PATH_MULTI, MOE_PATH_DECODE, MOE_PATH_TC = 0, 1, 2, 3
 
 
@@ -72,6 +74,17 @@ class MoeCacheStats(ctypes.Structure):
     _fields_ = [("hits", ctypes.c_int64), ("misses", ctypes.c_int64), ("bytes", ctypes.c_int64)]
 
 
+class MoeGateRule(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_value", ctypes.c_int32), ("raw_weights", ctypes.c_int32)]
+
+
+class MoeAdapters(ctypes.Structure):
+    _fields_ = [("n_adapters", ctypes.c_int32), ("r_max", ctypes.c_int32), ("d_in", ctypes.c_int32),
+                ("d_out", ctypes.c_int32), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
+                ("rank", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
 def config(d: int, f: int, n_experts: int, top_k: int, has_shared: int = 1, wbits: int = 4,
            routed_scale: float = 2.5, tc_min_tokens: int = 0, topp: float = 0.0) -> MoeConfig:
     return MoeConfig(d, f, n_experts, top_k, has_shared, wbits, routed_scale, tc_min_tokens, topp)
@@ -83,7 +96,7 @@ def _load() -> ctypes.CDLL:
     L = ctypes.CDLL(LIB_PATH)
     P, I32, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
     C = ctypes.POINTER(MoeConfig)
-    PL = ctypes.POINTER(MoePool)
+    PL, R, I64 = ctypes.POINTER(MoePool), ctypes.POINTER(MoeGateRule), ctypes.c_int64
     sig = {
         "moe_workspace_bytes": (SZ, [C, I32]),
         "moe_workspace_init": (I32, [P, SZ, P]),
@@ -94,6 +107,12 @@ def _load() -> ctypes.CDLL:
         "moe_expert_down": (I32, [C, PL, I32, P, P, I32, P, P, P, SZ, P]),
         "moe_layer": (I32, [C, PL, P, P, P, I32, I32, P, I32, P, P, P, SZ, P]),
         "moe_layer_ex": (I32, [C, PL, P, P, P, I32, I32, P, I32, P, P, P, SZ, P, ctypes.POINTER(MoeLayerOpts)]),
+        "moe_gate": (I32, [C, R, P, I32, I64, I32, P, P, P, P]),
+        "moe_route_gated": (I32, [C, R, P, I32, I32, P, P, P, P, P, SZ, P]),
+        "moe_layer_routed": (I32, [C, PL, P, P, P, I32, I32, P, I32, P, SZ, P]),
+        "moe_adapter_plan_bytes": (SZ, [I32, I32]),
+        "moe_adapter_plan": (I32, [I32, P, I32, P, SZ, P]),
+        "moe_adapter": (I32, [ctypes.POINTER(MoeAdapters), P, SZ, P, I32, P, I64, I32, P, I64, P, I64, P]),
         "moe_rmsnorm": (I32, [P, I32, I32, I32, F, P, P, P]),
         "moe_poll_status": (I32, [P, ctypes.POINTER(I32), P]),
         "moe_cache_state_bytes": (SZ, [C, I32]),
@@ -300,6 +319,120 @@ def moe_layer(cfg: MoeConfig, pool: MoePool, w_router: torch.Tensor, bias: torch
         _check(lib.moe_layer_ex(*args, ctypes.byref(opts)), "moe_layer_ex")
 
 
+def gate_rule(score: str = "sigmoid", n_groups: int = 0, topk_groups: int = 0, group_value: str = "top2",
+              renorm: bool = True) -> MoeGateRule:
+    """A selection rule: ``score`` "sigmoid" or "softmax"; with ``n_groups`` > 1
+    a row selects from its ``topk_groups`` best groups, a group's value the sum
+    of its two largest ("top2") or its largest ("max"); ``renorm`` divides the
+    weights by their sum."""
+    return MoeGateRule({"sigmoid": MOE_SCORE_SIGMOID, "softmax": MOE_SCORE_SOFTMAX}[score], n_groups, topk_groups,
+                       {"top2": MOE_GROUP_TOP2, "max": MOE_GROUP_MAX}[group_value], 0 if renorm else 1)
+
+
+def _rows(t: torch.Tensor, d: int, name: str, dtype=None):
+    """Pointer and row stride of a [T][d] matrix whose rows may lie apart."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current device")
+    if t.dim() != 2 or t.shape[1] != d:
+        raise ValueError(f"{name}: expected [T][{d}], got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    ld, step = t.stride()
+    if step != 1 and d > 1:
+        raise ValueError(f"{name}: expected rows of neighbouring elements")
+    return t.data_ptr(), ld if t.shape[0] > 1 else max(ld, d)
+
+
+def moe_gate(cfg: MoeConfig, rule: MoeGateRule, logits: torch.Tensor, bias: Optional[torch.Tensor],
+             topk_idx: torch.Tensor, topk_w: torch.Tensor, stream=None):
+    """Selects experts from logits [T][E] (float32 or bfloat16; rows may be a
+    slice of a wider matrix): indices (-1: no expert) and weights."""
+    T = logits.shape[0]
+    p, ld = _rows(logits, cfg.n_experts, "logits")
+    _check(lib.moe_gate(ctypes.byref(cfg), ctypes.byref(rule), p, _xdtype(logits), ld, T,
+                        _ptr(bias, torch.float32, cfg.n_experts, "bias"),
+                        _ptr(topk_idx, torch.int32, T * cfg.top_k, "topk_idx"),
+                        _ptr(topk_w, torch.float32, T * cfg.top_k, "topk_w"), _stream(stream)), "moe_gate")
+
+
+def moe_route_gated(cfg: MoeConfig, rule: MoeGateRule, x: torch.Tensor, w_router: torch.Tensor,
+                    bias: Optional[torch.Tensor], topk_idx: torch.Tensor, topk_w: torch.Tensor, ws: torch.Tensor,
+                    stream=None):
+    """moe_route with the selection of moe_gate."""
+    T = x.shape[0]
+    _check(lib.moe_route_gated(ctypes.byref(cfg), ctypes.byref(rule), _ptr(x, None, T * cfg.d, "x"), _xdtype(x), T,
+                               _ptr(w_router, torch.float32, cfg.n_experts * cfg.d, "w_router"),
+                               _ptr(bias, torch.float32, cfg.n_experts, "bias"),
+                               _ptr(topk_idx, torch.int32, T * cfg.top_k, "topk_idx"),
+                               _ptr(topk_w, torch.float32, T * cfg.top_k, "topk_w"),
+                               _ptr(ws, torch.uint8, name="ws"), ws.numel(), _stream(stream)), "moe_route_gated")
+
+
+def moe_layer_routed(cfg: MoeConfig, pool: MoePool, topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
+                     out: torch.Tensor, ws: torch.Tensor, accumulate: bool = False, stream=None):
+    """moe_layer for a routing the caller has."""
+    T = x.shape[0]
+    _check(lib.moe_layer_routed(ctypes.byref(cfg), ctypes.byref(pool),
+                                _ptr(topk_idx, torch.int32, T * cfg.top_k, "topk_idx"),
+                                _ptr(topk_w, torch.float32, T * cfg.top_k, "topk_w"),
+                                _ptr(x, None, T * cfg.d, "x"), _xdtype(x), T,
+                                _ptr(out, torch.float32, T * cfg.d, "out"), 1 if accumulate else 0,
+                                _ptr(ws, torch.uint8, name="ws"), ws.numel(), _stream(stream)), "moe_layer_routed")
+
+
+def make_adapters(a: torch.Tensor, b: torch.Tensor, rank: Optional[torch.Tensor] = None,
+                  scale: Optional[torch.Tensor] = None) -> MoeAdapters:
+    """The C struct over ``a`` [n][r_max][d_in] and ``b`` [n][d_out][r_max]
+    (bfloat16), ``rank`` [n] (int32) and ``scale`` [n] (float32); it keeps
+    references to them."""
+    if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
+        raise ValueError(f"adapters: expected a [n][r][d_in] and b [n][d_out][r], got {list(a.shape)}, {list(b.shape)}")
+    n, r, d_in = a.shape
+    ad = MoeAdapters(n, r, d_in, b.shape[1], _ptr(a, torch.bfloat16, name="adapters.a"),
+                     _ptr(b, torch.bfloat16, name="adapters.b"), _ptr(rank, torch.int32, n, "adapters.rank"),
+                     _ptr(scale, torch.float32, n, "adapters.scale"))
+    ad._tensors = (a, b, rank, scale)
+    return ad
+
+
+def moe_adapter_plan_bytes(n_adapters: int, max_tokens: int) -> int:
+    n = lib.moe_adapter_plan_bytes(n_adapters, max_tokens)
+    if n == 0:
+        raise MoeError(MOE_EINVAL, "moe_adapter_plan_bytes", lib.moe_last_error().decode())
+    return n
+
+
+def moe_adapter_plan(n_adapters: int, adapter_of: torch.Tensor, plan: torch.Tensor, stream=None):
+    _check(lib.moe_adapter_plan(n_adapters, _ptr(adapter_of, torch.int32, name="adapter_of"), adapter_of.numel(),
+                                _ptr(plan, torch.uint8, name="plan"), plan.numel(), _stream(stream)),
+           "moe_adapter_plan")
+
+
+def adapter_plan(n_adapters: int, adapter_of: torch.Tensor, stream=None) -> torch.Tensor:
+    """Allocate (through torch) and make the plan of a batch."""
+    plan = torch.empty(moe_adapter_plan_bytes(n_adapters, adapter_of.numel()), dtype=torch.uint8,
+                       device=adapter_of.device)
+    moe_adapter_plan(n_adapters, adapter_of, plan, stream)
+    return plan
+
+
+def moe_adapter(ad: MoeAdapters, plan: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
+                base: Optional[torch.Tensor] = None, sx: Optional[torch.Tensor] = None, stream=None):
+    """y = base + the rows' adapters of x (float32, bfloat16, or int8 codes
+    with ``sx``); ``base`` may be ``y``; rows may lie apart."""
+    T = x.shape[0]
+    xp, ldx = _rows(x, ad.d_in, "x")
+    yp, ldy = _rows(y, ad.d_out, "y", torch.float32)
+    bp, ldb = _rows(base, ad.d_out, "base", torch.float32) if base is not None else (None, 0)
+    if y.shape[0] != T or (base is not None and base.shape[0] != T):
+        raise ValueError(f"x, y and base: expected {T} rows each")
+    _check(lib.moe_adapter(ctypes.byref(ad), _ptr(plan, torch.uint8, name="plan"), plan.numel(), xp,
+                           MOE_I8 if x.dtype == torch.int8 else _xdtype(x), _ptr(sx, torch.float32, T, "sx"), ldx, T,
+                           bp, ldb, yp, ldy, _stream(stream)), "moe_adapter")
+
+
 def moe_rmsnorm(x: torch.Tensor, x_in: torch.Tensor, eps: float = 1e-6, x_copy=None, stream=None):
     T, d = x.shape
     _check(lib.moe_rmsnorm(_ptr(x, name="x"), _xdtype(x), T, d, eps, _ptr(x_in, torch.float32, T * d, "x_in"),
@@ -312,5 +445,7 @@ def moe_poll_status(ws: torch.Tensor, stream=None) -> int:
     return st
 
 
-__all__ = [n for n in dir() if n.startswith("moe_")] + ["MoeConfig", "MoePool", "MoeLayerOpts", "MoeError", "config",
-                                                         "make_pool", "workspace", "lib"]
+__all__ = [n for n in dir() if n.startswith("moe_")] + ["MoeConfig", "MoePool", "MoeLayerOpts", "MoeGateRule",
+                                                         "MoeAdapters", "MoeError", "config", "make_pool",
+                                                         "gate_rule", "make_adapters", "adapter_plan", "workspace",
+                                                         "lib"]

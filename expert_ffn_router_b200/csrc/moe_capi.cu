@@ -218,10 +218,11 @@ static moe_status check_ws(const moe_config* c, int T, void* ws, size_t ws_bytes
 }
 
 // ---------------------------------------------------------------------------
-// router launch sequence (a0 + a1 (+ a2))
+// router launch sequence (a0 + a1 (+ a2)); logits_only: the logits' p.ksplit
+// planes in the workspace and nothing after them
 // ---------------------------------------------------------------------------
 template <int TM, typename XT>
-static cudaError_t route_small_nv(Params& p, const XT* x, int do_quant, int bucket, cudaStream_t s) {
+static cudaError_t route_small_nv(Params& p, const XT* x, int do_quant, int bucket, int logits_only, cudaStream_t s) {
     const int E = p.m.E;
     const size_t smem = std::max((size_t)2 * kWarps * E * 4, (size_t)bucket_smem_ints(E) * 4);
     const int nv = p.m.d / 4;
@@ -232,7 +233,7 @@ static cudaError_t route_small_nv(Params& p, const XT* x, int do_quant, int buck
         auto fn = k_route_small<TM, NV, XT>;                                         \
         cudaError_t e = allow_smem((const void*)fn, smem);                           \
         if (e != cudaSuccess) return e;                                              \
-        fn<<<grid, kThreads, smem, s>>>(p, x, do_quant, bucket);                     \
+        fn<<<grid, kThreads, smem, s>>>(p, x, do_quant, bucket, logits_only);        \
         return cudaGetLastError();                                                   \
     }
     if (per <= 2) MOE_RS(2)
@@ -242,15 +243,15 @@ static cudaError_t route_small_nv(Params& p, const XT* x, int do_quant, int buck
 }
 
 template <typename XT>
-static cudaError_t launch_router(Params& p, const XT* x, int do_quant, int bucket, cudaStream_t s) {
+static cudaError_t launch_router(Params& p, const XT* x, int do_quant, int bucket, int logits_only, cudaStream_t s) {
     const int T = p.m.T, E = p.m.E, d = p.m.d;
     if (T <= 8) {
         p.ksplit = 1;
         switch (T <= 1 ? 1 : T <= 2 ? 2 : T <= 4 ? 4 : 8) {
-            case 1: return route_small_nv<1>(p, x, do_quant, bucket, s);
-            case 2: return route_small_nv<2>(p, x, do_quant, bucket, s);
-            case 4: return route_small_nv<4>(p, x, do_quant, bucket, s);
-            default: return route_small_nv<8>(p, x, do_quant, bucket, s);
+            case 1: return route_small_nv<1>(p, x, do_quant, bucket, logits_only, s);
+            case 2: return route_small_nv<2>(p, x, do_quant, bucket, logits_only, s);
+            case 4: return route_small_nv<4>(p, x, do_quant, bucket, logits_only, s);
+            default: return route_small_nv<8>(p, x, do_quant, bucket, logits_only, s);
         }
     }
     cudaError_t e;
@@ -268,7 +269,7 @@ static cudaError_t launch_router(Params& p, const XT* x, int do_quant, int bucke
     ks = (ksteps + per - 1) / per;
     p.ksplit = ks;
     k_router_tiled<XT><<<dim3((E + 63) / 64, (T + 63) / 64, ks), kThreads, 0, s>>>(p, x);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = cudaGetLastError()) != cudaSuccess || logits_only) return e;
     if (E <= 256) {  // register top-k; its last CTA buckets
         const size_t smem_b = bucket ? (size_t)bucket_smem_ints(E) * 4 : 0;
         if ((e = allow_smem((const void*)k_topk_small, smem_b)) != cudaSuccess) return e;
@@ -289,8 +290,13 @@ static cudaError_t launch_router(Params& p, const XT* x, int do_quant, int bucke
 }
 
 cudaError_t launch_router_any(Params& p, const void* x, moe_dtype dt, int do_quant, int bucket, cudaStream_t s) {
-    if (dt == MOE_BF16) return launch_router(p, static_cast<const __nv_bfloat16*>(x), do_quant, bucket, s);
-    return launch_router(p, static_cast<const float*>(x), do_quant, bucket, s);
+    if (dt == MOE_BF16) return launch_router(p, static_cast<const __nv_bfloat16*>(x), do_quant, bucket, 0, s);
+    return launch_router(p, static_cast<const float*>(x), do_quant, bucket, 0, s);
+}
+
+static cudaError_t launch_logits(Params& p, const void* x, moe_dtype dt, cudaStream_t s) {
+    if (dt == MOE_BF16) return launch_router(p, static_cast<const __nv_bfloat16*>(x), 0, 0, 1, s);
+    return launch_router(p, static_cast<const float*>(x), 0, 0, 1, s);
 }
 
 moe_status check_dtype(moe_dtype dt) {
@@ -626,6 +632,97 @@ moe_status moe_layer(const moe_config* cfg, const moe_pool* pool, const float* w
                      float* topk_w_out, void* ws, size_t ws_bytes, moe_stream_t stream) {
     return moe_layer_ex(cfg, pool, w_router, bias, x, dtype, T, out, accumulate, topk_idx_out, topk_w_out, ws,
                         ws_bytes, stream, nullptr);
+}
+
+moe_status moe_route_gated(const moe_config* cfg, const moe_gate_rule* rule, const void* x, moe_dtype dtype, int32_t T,
+                           const float* w_router, const float* bias, int32_t* topk_idx, float* topk_w, void* ws,
+                           size_t ws_bytes, moe_stream_t stream) {
+    MOE_TRY(check_cfg(cfg));
+    MOE_TRY(check_rule(cfg, rule));
+    MOE_TRY(check_dtype(dtype));
+    if (T < 0) return fail(MOE_EINVAL, "T < 0");
+    if (T == 0) return MOE_OK;
+    MOE_TRY(check_ptr(x, "x"));
+    MOE_TRY(check_ptr(w_router, "w_router"));
+    MOE_TRY(check_ptr(bias, "bias", true));
+    MOE_TRY(check_ptr(topk_idx, "topk_idx"));
+    MOE_TRY(check_ptr(topk_w, "topk_w"));
+    const Dims m = dims_of(cfg, T, cfg->top_k + cfg->has_shared);
+    MOE_TRY(check_ws(cfg, T, ws, ws_bytes));
+    Params p = base_params(cfg, m, ws, ws_bytes);
+    p.w_router = w_router;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = launch_logits(p, x, dtype, s);
+    if (e == cudaSuccess)
+        e = launch_gate(cfg, rule, p.ws.logits, MOE_F32, cfg->n_experts, p.ksplit, (long long)T * cfg->n_experts, T,
+                        bias, topk_idx, topk_w, s);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_route_gated");
+}
+
+moe_status moe_layer_routed(const moe_config* cfg, const moe_pool* pool, const int32_t* topk_idx, const float* topk_w,
+                            const void* x, moe_dtype dtype, int32_t T, float* out, int32_t accumulate, void* ws,
+                            size_t ws_bytes, moe_stream_t stream) {
+    MOE_TRY(check_cfg(cfg));
+    MOE_TRY(check_dtype(dtype));
+    if (!pool) return fail(MOE_EINVAL, "pool is NULL");
+    if (T < 0) return fail(MOE_EINVAL, "T < 0");
+    if (T == 0) return MOE_OK;
+    MOE_TRY(check_ptr(pool->w, "pool->w"));
+    MOE_TRY(check_pool_slots(pool));
+    MOE_TRY(check_ptr(pool->s, "pool->s"));
+    MOE_TRY(check_ptr(topk_idx, "topk_idx"));
+    MOE_TRY(check_ptr(topk_w, "topk_w"));
+    MOE_TRY(check_ptr(x, "x"));
+    MOE_TRY(check_ptr(out, "out"));
+    const Dims m = dims_of(cfg, T, cfg->top_k + cfg->has_shared);
+    MOE_TRY(check_ws(cfg, T, ws, ws_bytes));
+    const bool tc = use_tc(cfg, T);
+    Params p = base_params(cfg, m, ws, ws_bytes, tc);
+    p.pool = pool->w;
+    p.scales = pool->s;
+    p.slot_of = pool->slot_of;
+    p.n_slots = pool->n_slots;
+    p.out = out;
+    p.accumulate = accumulate ? 1 : 0;
+    // a token may name one expert several times: a task holds up to T * top_k rows
+    const int nt_max = tc_npad((int)std::min((long long)T * cfg->top_k, (long long)kTcNT));
+    cudaStream_t s = (cudaStream_t)stream;
+    const int quant_grid = std::min((int)T, 65535);
+    if (dtype == MOE_BF16)
+        k_quantize<__nv_bfloat16><<<quant_grid, kThreads, 0, s>>>(static_cast<const __nv_bfloat16*>(x), T, cfg->d,
+                                                                   p.ws.xq, p.ws.sx, p.ws.xcs);
+    else
+        k_quantize<float><<<quant_grid, kThreads, 0, s>>>(static_cast<const float*>(x), T, cfg->d, p.ws.xq, p.ws.sx,
+                                                          p.ws.xcs);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) {
+        k_take_routing<<<std::min((T * cfg->top_k + kThreads - 1) / kThreads, 592), kThreads, 0, s>>>(p, topk_idx,
+                                                                                                    topk_w);
+        e = cudaGetLastError();
+    }
+    const size_t smem_b = (size_t)bucket_smem_ints(cfg->n_experts) * 4;
+    if (e == cudaSuccess) e = allow_smem((const void*)k_bucket, smem_b);
+    if (e == cudaSuccess) {
+        k_bucket<<<1, kThreads, smem_b, s>>>(p);
+        e = cudaGetLastError();
+    }
+    if (tc) {
+        if (e == cudaSuccess) e = launch_tc_gather(p, p.ws.xq, cfg->d, m.S, cfg->d, p.ws.xb, s);
+        if (e == cudaSuccess) e = launch_tc_expert(p, 0, nt_max, s);
+        if (e == cudaSuccess) e = launch_tc_requant(p, s);
+        if (e == cudaSuccess) e = launch_tc_expert(p, 1, nt_max, s);
+        if (e == cudaSuccess) e = launch_combine(p, s);
+        return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_layer_routed (tensor cores)");
+    }
+    // the dp4a down kernel writes the output as the last task of a row block
+    // arrives: a batch without any task (no shared expert, every slot empty)
+    // would leave it unwritten, so it starts at zero
+    if (e == cudaSuccess && !cfg->has_shared && !accumulate)
+        e = cudaMemsetAsync(out, 0, (size_t)T * cfg->d * sizeof(float), s);
+    const ExpertTiling tl = expert_tiling(cfg->d, cfg->f, cfg->wbits);
+    if (e == cudaSuccess) e = launch_gate_up(p, tl, false, s);
+    if (e == cudaSuccess) e = launch_down(p, tl, false, s);
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_layer_routed");
 }
 
 moe_status moe_rmsnorm(const void* x, moe_dtype dtype, int32_t T, int32_t d, float eps, float* x_in, float* x_copy,

@@ -1,0 +1,88 @@
+// moe_gate: argument checks and launch of the expert selection.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <string>
+
+#include "moe.h"
+#include "moe_gate.cuh"
+#include "moe_launch.h"
+
+namespace moe {
+
+moe_status check_rule(const moe_config* c, const moe_gate_rule* r) {
+    if (!r) return fail(MOE_EINVAL, "rule is NULL");
+    if (r->score != MOE_SCORE_SIGMOID && r->score != MOE_SCORE_SOFTMAX)
+        return fail(MOE_EINVAL, "rule->score must be MOE_SCORE_SIGMOID or MOE_SCORE_SOFTMAX");
+    if (r->raw_weights != 0 && r->raw_weights != 1) return fail(MOE_EINVAL, "rule->raw_weights must be 0 or 1");
+    if (r->n_groups < 0 || r->n_groups > 32) return fail(MOE_EINVAL, "rule->n_groups must be in [0, 32]");
+    if (r->n_groups <= 1) return MOE_OK;
+    if (c->n_experts % r->n_groups) return fail(MOE_EINVAL, "rule->n_groups must divide n_experts");
+    if (r->topk_groups < 1 || r->topk_groups > r->n_groups)
+        return fail(MOE_EINVAL, "rule->topk_groups must be in [1, n_groups]");
+    if (r->group_value != MOE_GROUP_TOP2 && r->group_value != MOE_GROUP_MAX)
+        return fail(MOE_EINVAL, "rule->group_value must be MOE_GROUP_TOP2 or MOE_GROUP_MAX");
+    if (c->top_k > r->topk_groups * (c->n_experts / r->n_groups))
+        return fail(MOE_EINVAL, "top_k exceeds the experts of topk_groups groups");
+    return MOE_OK;
+}
+
+template <typename LT>
+static cudaError_t launch_gate_t(const GateArgs& a, cudaStream_t s) {
+    const size_t smem = (size_t)kWarps * a.E * sizeof(double);
+    const void* fn = (const void*)k_gate<LT>;
+    cudaError_t e = allow_smem(fn, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = std::min((a.T + kWarps - 1) / kWarps, persistent_grid(fn, smem));
+    k_gate<LT><<<grid, kThreads, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_gate(const moe_config* c, const moe_gate_rule* r, const void* logits, moe_dtype dt, long long ld,
+                        int nplanes, long long plane, int T, const float* bias, int32_t* idx, float* w,
+                        cudaStream_t s) {
+    GateArgs a{};
+    a.logits = logits;
+    a.ld = ld;
+    a.plane = plane;
+    a.nplanes = nplanes;
+    a.bias = bias;
+    a.T = T;
+    a.E = c->n_experts;
+    a.k = c->top_k;
+    a.softmax = r->score == MOE_SCORE_SOFTMAX;
+    a.G = std::max(1, (int)r->n_groups);
+    a.gs = a.E / a.G;
+    a.keep = a.G > 1 ? r->topk_groups : 1;
+    a.gmax = r->group_value == MOE_GROUP_MAX;
+    a.raw = r->raw_weights;
+    a.scale = c->routed_scale;
+    a.topp = c->topp;
+    a.idx = idx;
+    a.w = w;
+    return dt == MOE_BF16 ? launch_gate_t<__nv_bfloat16>(a, s) : launch_gate_t<float>(a, s);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_gate(const moe_config* cfg, const moe_gate_rule* rule, const void* logits, moe_dtype dtype,
+                               int64_t ld, int32_t T, const float* bias, int32_t* topk_idx, float* topk_w,
+                               moe_stream_t stream) {
+    moe_status st = check_cfg(cfg);
+    if (st != MOE_OK) return st;
+    if ((st = check_rule(cfg, rule)) != MOE_OK) return st;
+    if ((st = check_dtype(dtype)) != MOE_OK) return st;
+    if (T < 0) return fail(MOE_EINVAL, "T < 0");
+    if (ld < cfg->n_experts) return fail(MOE_EINVAL, "ld is smaller than n_experts");
+    if (T == 0) return MOE_OK;
+    if ((st = check_ptr(logits, "logits")) != MOE_OK) return st;
+    if ((st = check_ptr(bias, "bias", true)) != MOE_OK) return st;
+    if ((st = check_ptr(topk_idx, "topk_idx")) != MOE_OK) return st;
+    if ((st = check_ptr(topk_w, "topk_w")) != MOE_OK) return st;
+    const cudaError_t e = launch_gate(cfg, rule, logits, dtype, ld, 1, 0, T, bias, topk_idx, topk_w,
+                                      (cudaStream_t)stream);
+    return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, std::string("moe_gate: ") + cudaGetErrorString(e));
+}

@@ -41,6 +41,13 @@ moe_status check_ptr(const void* p, const char* name, bool nullable = false);
 moe_status check_dtype(moe_dtype dt);
 cudaError_t launch_down(const Params& p, const ExpertTiling& tl, bool dbg, cudaStream_t s);
 
+// Expert selection from logits (moe_gate.cu): logits [nplanes][T][E] with rows
+// ld and planes `plane` elements apart.
+moe_status check_rule(const moe_config* c, const moe_gate_rule* r);
+cudaError_t launch_gate(const moe_config* c, const moe_gate_rule* r, const void* logits, moe_dtype dt, long long ld,
+                        int nplanes, long long plane, int T, const float* bias, int32_t* idx, float* w,
+                        cudaStream_t s);
+
 // Tensor-core expert path (moe_ktc.cu).  nt_max: bound on the tokens of one
 // task in this call (<= kTcNT).
 bool tc_shape_ok(const Dims& m);

@@ -279,11 +279,12 @@ static __device__ void bucket_cta(const Params& p, int* smem) {
 // Router GEMV for up to TM tokens.  CTA b computes the logits of experts 2b and
 // 2b+1 for every token (each thread a slice of d, weights streamed once); CTAs
 // b < T also quantise token b.  The last CTA to finish runs the top-k of every
-// token (one warp per token) and, if `bucket`, the bucketing.
+// token (one warp per token) and, if `bucket`, the bucketing.  logits_only:
+// nothing after the logits.
 // Dynamic smem: max(2 * kWarps * E floats, bucket_smem_ints(E) ints).
 template <int TM, int NV, typename XT>
 __global__ void __launch_bounds__(kThreads) k_route_small(const Params p, const XT* __restrict__ x,
-                                                          int do_quant, int bucket) {
+                                                          int do_quant, int bucket, int logits_only) {
     extern __shared__ float dsm[];
     __shared__ float redf[kWarps];
     __shared__ int redi[kWarps];
@@ -347,6 +348,7 @@ __global__ void __launch_bounds__(kThreads) k_route_small(const Params p, const 
             p.ws.logits[(size_t)t * E + e0 + j] = v;
         }
     }
+    if (logits_only) return;
     // last-arriving CTA: top-k (+ bucketing) over every token
     __syncthreads();
     if (tid == 0) {
@@ -542,6 +544,22 @@ __global__ void __launch_bounds__(kThreads) k_topk_small(const Params p, int buc
     __threadfence();
     if (tid == 0) p.ws.hdr->route_ctr = 0u;
     bucket_cta(p, bsm);
+}
+
+// A routing given by the caller into the workspace: a slot with index -1, or
+// with an index that is no expert's (recorded as MOE_EDEVICE), selects none.
+__global__ void __launch_bounds__(kThreads) k_take_routing(const Params p, const int32_t* __restrict__ idx,
+                                                           const float* __restrict__ w) {
+    const int n = p.m.T * p.m.k;
+    for (int i = blockIdx.x * kThreads + threadIdx.x; i < n; i += gridDim.x * kThreads) {
+        int e = idx[i];
+        if (e < -1 || e >= p.m.E) {
+            set_status(p.ws.hdr, MOE_EDEVICE, i);
+            e = -1;
+        }
+        p.ws.idx[i] = e;
+        p.ws.w[i] = e < 0 ? 0.0f : w[i];
+    }
 }
 
 // Bucketing alone (one CTA).  Dynamic smem bucket_smem_ints(E) ints.

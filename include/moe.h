@@ -69,7 +69,8 @@ typedef enum {
     MOE_EDEVICE = -6   /* a kernel found an invalid value, e.g. an index out of range */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+/* MOE_I8: int8 codes with a float32 scale per row, taken by moe_adapter only. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_I8 = 2 } moe_dtype;
 
 /* Shape of one MoE layer.
  *  d: hidden size; f: expert intermediate size; n_experts: routed experts E;
@@ -265,6 +266,128 @@ MOE_API moe_status moe_layer_ex(const moe_config* cfg, const moe_pool* pool, con
  * stream from bf16 activations). */
 MOE_API moe_status moe_rmsnorm(const void* x, moe_dtype dtype, int32_t T, int32_t d, float eps, float* x_in,
                        float* x_copy, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Expert selection from router logits.
+ *
+ * moe_route computes one rule (sigmoid scores plus bias, any expert, weights
+ * renormalised) on logits that it keeps to itself.  moe_gate takes the logits
+ * of any router and selects by a moe_gate_rule; a zero-initialised rule is
+ * moe_route's.  For a row l[0..E) of logits and a bias b[0..E) (NULL: none):
+ *  - an expert can be selected unless its logit or its bias is NaN or -inf
+ *    (a caller masks experts by logits of -inf);
+ *  - score s_e = 1 / (1 + exp(-l_e)) (MOE_SCORE_SIGMOID), or
+ *    exp(l_e - max l) / sum exp(l - max l) over the selectable experts
+ *    (MOE_SCORE_SOFTMAX);
+ *  - with n_groups > 1 the experts form n_groups groups of E / n_groups
+ *    neighbours.  A group counts as the sum of its two largest s_e + b_e
+ *    (MOE_GROUP_TOP2; its only one, where a single expert can be selected) or
+ *    as its largest (MOE_GROUP_MAX).  The topk_groups largest groups stay,
+ *    the lower group first on ties; a group without a selectable expert never
+ *    does;
+ *  - the top_k largest s_e + b_e of the groups that stay, descending, ties to
+ *    the lower expert index.  Without a bias the order is that of the logits;
+ *  - a slot that no expert is left for gets index -1 and weight 0 (a row may
+ *    have only such slots);
+ *  - cfg->topp truncates as in moe_config, on the scores of the selected slots;
+ *  - weight = score / (sum of the kept scores) * routed_scale; with
+ *    raw_weights score * routed_scale.  Scores whose sum is 0 give weights 0.
+ * Scores, group values, selection values and the truncation's sums are
+ * compared as double precision gives them, so near-equal experts take the
+ * same order on every path of the kernel; logits of one value tie exactly.
+ * Limits (MOE_EINVAL otherwise): n_groups <= 32, a divisor of n_experts;
+ * 1 <= topk_groups <= n_groups; top_k <= topk_groups * n_experts / n_groups.
+ * n_groups 0 or 1: no groups, topk_groups and group_value are not read.  Of
+ * cfg only n_experts, top_k, routed_scale and topp are used.
+ * ------------------------------------------------------------------------- */
+enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
+enum { MOE_GROUP_TOP2 = 0, MOE_GROUP_MAX = 1 };
+typedef struct {
+    int32_t score;       /* MOE_SCORE_* */
+    int32_t n_groups;    /* 0 or 1: no groups */
+    int32_t topk_groups; /* groups a row selects from */
+    int32_t group_value; /* MOE_GROUP_* */
+    int32_t raw_weights; /* 1: weights are not renormalised */
+} moe_gate_rule;
+
+/* logits [T][E] (MOE_F32 or MOE_BF16), rows ld >= E elements apart; bias fp32
+ * [E] or NULL -> topk_idx int32 [T][top_k], topk_w fp32 [T][top_k], as
+ * moe_route writes them.  No workspace. */
+MOE_API moe_status moe_gate(const moe_config* cfg, const moe_gate_rule* rule, const void* logits, moe_dtype dtype,
+                            int64_t ld, int32_t T, const float* bias, int32_t* topk_idx, float* topk_w,
+                            moe_stream_t stream);
+
+/* moe_route with a rule: moe_route's projection (fp32 logits of x), then the
+ * selection of moe_gate on them.  bias may be NULL. */
+MOE_API moe_status moe_route_gated(const moe_config* cfg, const moe_gate_rule* rule, const void* x, moe_dtype dtype,
+                                   int32_t T, const float* w_router, const float* bias, int32_t* topk_idx,
+                                   float* topk_w, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* moe_layer for a routing that the caller has (of moe_gate, moe_route_gated,
+ * or its own): topk_idx int32 [T][top_k] and topk_w fp32 [T][top_k] are
+ * inputs.  A slot with index -1 selects no expert, whatever its weight; any
+ * other index outside [0, n_experts) is recorded as MOE_EDEVICE in the status
+ * word and its slot dropped.  The same expert may stand in several slots of a
+ * token.  A row without any expert gets the shared expert's output alone (or
+ * zeros). */
+MOE_API moe_status moe_layer_routed(const moe_config* cfg, const moe_pool* pool, const int32_t* topk_idx,
+                                    const float* topk_w, const void* x, moe_dtype dtype, int32_t T, float* out,
+                                    int32_t accumulate, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection.
+ *
+ * The requests of a batch share the projections (moe_expert_down,
+ * moe_expert_ffn, moe_layer, or any other); each request may bring a low-rank
+ * update of its own.  With a = the adapter of row t,
+ *     y[t] = base[t] + scale[a] * B[a] (A[a] x[t])
+ * and y[t] = base[t] for a row without an adapter.  All sums are float32; the
+ * products are exact (bf16 weights; float32 x and the rank-long vector A x are
+ * each split into three bf16 parts that hold all 24 bits).  A row with a value
+ * that is not finite gives a row that is not finite; no row reaches another.
+ *
+ * Which rows belong to which adapter is the batch's plan.  It depends on
+ * adapter_of alone: moe_adapter_plan makes it once on the device, and every
+ * moe_adapter call of the step (any layer, any projection) reads it.
+ * ------------------------------------------------------------------------- */
+
+/* n_adapters adapters in device memory:
+ *  a: bf16 [n_adapters][r_max][d_in], b: bf16 [n_adapters][d_out][r_max];
+ *  rank: int32 [n_adapters], or NULL (every rank is r_max): rows of a[i] and
+ *     columns of b[i] from rank[i] on take no part, whatever they hold; a rank
+ *     outside [0, r_max] is clamped to it;
+ *  scale: fp32 [n_adapters], or NULL (1).
+ * Limits (MOE_EINVAL otherwise): 1 <= n_adapters <= 1024; r_max in [8, 128], a
+ * multiple of 8; d_in and d_out in [16, 32768], multiples of 16. */
+typedef struct {
+    int32_t n_adapters, r_max, d_in, d_out;
+    const void* a;
+    const void* b;
+    const int32_t* rank;
+    const float* scale;
+} moe_adapters;
+
+/* Bytes of the plan of up to max_tokens rows (0: an argument out of range). */
+MOE_API size_t moe_adapter_plan_bytes(int32_t n_adapters, int32_t max_tokens);
+
+/* adapter_of int32 [T] (device; -1: no adapter) -> plan.  An entry outside
+ * [-1, n_adapters) is recorded as MOE_EDEVICE in the plan's status word
+ * (moe_poll_status(plan, ...)) and counts as -1.  The order of the rows of an
+ * adapter is theirs in the batch. */
+MOE_API moe_status moe_adapter_plan(int32_t n_adapters, const int32_t* adapter_of, int32_t T, void* plan,
+                                    size_t plan_bytes, moe_stream_t stream);
+
+/* x [T][d_in] (dtype MOE_F32, MOE_BF16, or MOE_I8 with sx fp32 [T]: x = code *
+ * sx), rows ldx elements apart (16-byte aligned rows); base and y fp32
+ * [T][d_out], rows ldbase and ldy elements apart (multiples of 4).  base NULL:
+ * y[t] = the update alone (0 without an adapter).  base may be y (in place,
+ * with ldbase = ldy); otherwise y must overlap none of the inputs.  T must be
+ * the plan's, n_adapters too: a mismatch is recorded as MOE_EDEVICE in the
+ * plan's status word and nothing is written.  No workspace: calls on one plan
+ * may overlap.  Rows from T on are left as they are. */
+MOE_API moe_status moe_adapter(const moe_adapters* ad, void* plan, size_t plan_bytes, const void* x,
+                               moe_dtype dtype, const float* sx, int64_t ldx, int32_t T, const float* base,
+                               int64_t ldbase, float* y, int64_t ldy, moe_stream_t stream);
 
 /* Device-side status word of a workspace (MOE_OK if no kernel reported an
  * error).  Synchronises `stream` first.  *info (optional) receives a detail
