@@ -30,10 +30,40 @@ static bool overlap(const void* p, size_t np, const void* q, size_t nq) {
     return p && q && a < b + nq && b < a + np;
 }
 
+// CTAs of a task's cluster.
+static int cluster_size(const AdArgs& g) {
+    const int units = std::max(g.d_in / 32, g.d_out / 16);
+    return units >= 64 ? 8 : units >= 32 ? 4 : units >= 16 ? 2 : 1;
+}
+
+template <typename XT, int RT>
+static cudaError_t launch_adapter_rt(const AdArgs& g, cudaStream_t s) {
+    auto fn = k_adapter<XT, RT>;
+    const size_t smem = sizeof(AdSmem<RT>);
+    cudaError_t e = allow_smem((const void*)fn, smem);
+    if (e != cudaSuccess) return e;
+    const int cs = cluster_size(g);
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3((unsigned)(cs * ad_max_tasks(g.n, g.T)));
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cs;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    c.attrs = at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, fn, g);
+}
+
 template <typename XT>
 static cudaError_t launch_adapter(const AdArgs& g, cudaStream_t s) {
-    k_adapter<XT><<<ad_max_tasks(g.n, g.T), kThreads, 0, s>>>(g);
-    return cudaGetLastError();
+    if (g.r_max <= 16) return launch_adapter_rt<XT, 16>(g, s);
+    if (g.r_max <= 32) return launch_adapter_rt<XT, 32>(g, s);
+    if (g.r_max <= 64) return launch_adapter_rt<XT, 64>(g, s);
+    return launch_adapter_rt<XT, 128>(g, s);
 }
 
 }  // namespace moe
