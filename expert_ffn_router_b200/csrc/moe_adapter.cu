@@ -3,7 +3,10 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <map>
+#include <mutex>
 #include <string>
+#include <tuple>
 
 #include "moe.h"
 #include "moe_adapter.cuh"
@@ -36,15 +39,31 @@ static int cluster_size(const AdArgs& g) {
     return units >= 64 ? 8 : units >= 32 ? 4 : units >= 16 ? 2 : 1;
 }
 
-template <typename XT, int RT>
-static cudaError_t launch_adapter_rt(const AdArgs& g, cudaStream_t s) {
-    auto fn = k_adapter<XT, RT>;
-    const size_t smem = sizeof(AdSmem<RT>);
+// Clusters of cs CTAs that the device holds at once (cached per kernel).
+static int resident_clusters(const void* fn, const cudaLaunchConfig_t& c, int cs) {
+    static std::mutex mu;
+    static std::map<std::tuple<int, const void*, int>, int> known;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const auto key = std::make_tuple(dev, fn, cs);
+    std::lock_guard<std::mutex> lk(mu);
+    auto it = known.find(key);
+    if (it != known.end()) return it->second;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, fn, &c) != cudaSuccess || n < 1) return 1;
+    known[key] = n;
+    return n;
+}
+
+template <typename XT, int RT, int MR>
+static cudaError_t launch_adapter_t(const AdArgs& g, cudaStream_t s) {
+    auto fn = k_adapter<XT, RT, MR>;
+    const size_t smem = AdTile<XT, RT, MR>::SMEM;
     cudaError_t e = allow_smem((const void*)fn, smem);
     if (e != cudaSuccess) return e;
     const int cs = cluster_size(g);
     cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)(cs * ad_max_tasks(g.n, g.T)));
+    c.gridDim = dim3((unsigned)cs);
     c.blockDim = dim3(kThreads);
     c.dynamicSmemBytes = smem;
     c.stream = s;
@@ -55,7 +74,15 @@ static cudaError_t launch_adapter_rt(const AdArgs& g, cudaStream_t s) {
     at[0].val.clusterDim.z = 1;
     c.attrs = at;
     c.numAttrs = 1;
+    const int tasks = ad_max_tasks(g.n, g.T, AdTile<XT, RT, MR>::LIST);
+    c.gridDim.x = (unsigned)(cs * std::min(tasks, resident_clusters((const void*)fn, c, cs)));
     return cudaLaunchKernelEx(&c, fn, g);
+}
+
+template <typename XT, int RT>
+static cudaError_t launch_adapter_rt(const AdArgs& g, cudaStream_t s) {
+    if (g.T < 1024) return launch_adapter_t<XT, RT, 16>(g, s);
+    return launch_adapter_t<XT, RT, 64>(g, s);
 }
 
 template <typename XT>

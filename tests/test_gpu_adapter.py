@@ -180,24 +180,27 @@ def test_large_and_tiny_values():
 
 
 def test_plan():
-    """Rows grouped by adapter in their order, tasks of at most 64."""
+    """Rows grouped by adapter in their order, tasks of at most 16 and of at most 64."""
     for T, n in ((1, 1), (64, 2), (65, 1), (1000, 7), (5000, 300), (3000, 1024), (0, 3)):
         of = owners(T, n, "mixed") if T else torch.empty(0, dtype=torch.int32, device="cuda")
         plan = M.adapter_plan(n, of).cpu()
         head = plan[:64].view(torch.int32)
         order = plan[64:64 + 4 * T].view(torch.int32)
-        at = (64 + 4 * T + 15) // 16 * 16
-        tasks = plan[at:at + 16 * int(head[5])].view(torch.int32).view(-1, 4).tolist()
         assert head[0] == 0 and head[3] == T and head[4] == n
         key = of.cpu().clone()
         key[key < 0] = n
         assert order.tolist() == key.sort(stable=True)[1].tolist()
-        seen = 0
-        for a, first, cnt, _ in tasks:
-            assert first == seen and 1 <= cnt <= 64
-            assert (of.cpu()[order[first:first + cnt].long()] == a).all()
-            seen += cnt
-        assert seen == T
+        at = (64 + 4 * T + 15) // 16 * 16
+        for i, most in enumerate((16, 64)):
+            tasks = plan[at:at + 16 * int(head[5 + i])].view(torch.int32).view(-1, 4).tolist()
+            at += 16 * (min(T, n + 1) + T // most)
+            seen = 0
+            for a, first, cnt, _ in tasks:
+                assert first == seen and 1 <= cnt <= most
+                assert (of.cpu()[order[first:first + cnt].long()] == a).all()
+                seen += cnt
+            assert seen == T
+        assert plan.numel() == at
 
 
 def test_bad_owner_is_recorded_and_counts_as_none():
