@@ -1,18 +1,31 @@
 // moe_adapter, moe_adapter_plan: argument checks and launches.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
-#include <map>
 #include <mutex>
 #include <string>
-#include <tuple>
+#include <type_traits>
 
 #include "moe.h"
 #include "moe_adapter.cuh"
+#include "moe_adapter_launch.h"
+#include "moe_adapter_plan.cuh"
 #include "moe_launch.h"
 
 namespace moe {
+
+// Which of the two kernels takes a call.  k_adapter (tasks of 64 rows on
+// tcgen05) needs long tasks and ranks that keep mma.sync busy; measured at
+// d = 6144, bf16 rows in runs, us with k_adapter_few and with k_adapter: rank 64,
+// 16 adapters, 2900 rows 97 and 64, 8192 rows 210 and 118; rank 16, 8192 rows 119
+// and 111, in fp32 144 and 204; rank 64, 64 adapters, rows mixed, 8192 rows 228
+// and 369.
+static bool ad_few(const AdArgs& g) {
+    return g.r_max <= 32 || g.T < 2048 || g.T / 256 < g.n;
+}
 
 static moe_status check_plan_args(int n_adapters, int T, const void* plan, size_t plan_bytes) {
     if (n_adapters < 1 || n_adapters > kAdMaxN) return fail(MOE_EINVAL, "n_adapters must be in [1, 1024]");
@@ -33,64 +46,66 @@ static bool overlap(const void* p, size_t np, const void* q, size_t nq) {
     return p && q && a < b + nq && b < a + np;
 }
 
-// CTAs of a task's cluster.
-static int cluster_size(const AdArgs& g) {
-    const int units = std::max(g.d_in / 32, g.d_out / 16);
-    return units >= 64 ? 8 : units >= 32 ? 4 : units >= 16 ? 2 : 1;
+// Tensor map of bf16 values, `rank` dimensions (the first one contiguous, the
+// others `pitch` bytes apart), zeros outside.
+static cudaError_t make_map(CUtensorMap* tm, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* pitch,
+                            const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    std::call_once(once, [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r = enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(p), dims, pitch, box, step,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Clusters of cs CTAs that the device holds at once (cached per kernel).
-static int resident_clusters(const void* fn, const cudaLaunchConfig_t& c, int cs) {
-    static std::mutex mu;
-    static std::map<std::tuple<int, const void*, int>, int> known;
-    int dev = 0;
-    cudaGetDevice(&dev);
-    const auto key = std::make_tuple(dev, fn, cs);
-    std::lock_guard<std::mutex> lk(mu);
-    auto it = known.find(key);
-    if (it != known.end()) return it->second;
-    int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, fn, &c) != cudaSuccess || n < 1) return 1;
-    known[key] = n;
-    return n;
-}
-
-template <typename XT, int RT, int MR>
-static cudaError_t launch_adapter_t(const AdArgs& g, cudaStream_t s) {
-    auto fn = k_adapter<XT, RT, MR>;
-    const size_t smem = AdTile<XT, RT, MR>::SMEM;
-    cudaError_t e = allow_smem((const void*)fn, smem);
+// A: rows of components, 64 columns x 16 rows a box.  B: outputs in pairs, 16
+// components x 128 outputs of one parity a box.  x (bf16): 64
+// columns of `rows` neighbouring rows, and of one.
+static cudaError_t make_maps(const AdArgs& g, bool x_bf16, int rows, CUtensorMap* a, CUtensorMap* b, CUtensorMap* x,
+                             CUtensorMap* x1) {
+    const cuuint64_t da[2] = {(cuuint64_t)g.d_in, (cuuint64_t)g.n * g.r_max}, pa[1] = {(cuuint64_t)g.d_in * 2};
+    const cuuint32_t ba[2] = {64, 16};
+    cudaError_t e = make_map(a, g.a, 2, da, pa, ba, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    const int cs = cluster_size(g);
-    cudaLaunchConfig_t c{};
-    c.gridDim = dim3((unsigned)cs);
-    c.blockDim = dim3(kThreads);
-    c.dynamicSmemBytes = smem;
-    c.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = (unsigned)cs;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    c.attrs = at;
-    c.numAttrs = 1;
-    const int tasks = ad_max_tasks(g.n, g.T, AdTile<XT, RT, MR>::LIST);
-    c.gridDim.x = (unsigned)(cs * std::min(tasks, resident_clusters((const void*)fn, c, cs)));
-    return cudaLaunchKernelEx(&c, fn, g);
+    const cuuint64_t db[3] = {(cuuint64_t)g.r_max, 2, (cuuint64_t)g.n * g.d_out / 2};
+    const cuuint64_t pb[2] = {(cuuint64_t)g.r_max * 2, (cuuint64_t)g.r_max * 4};
+    const cuuint32_t bb[3] = {16, 1, 128};
+    e = make_map(b, g.b, 3, db, pb, bb, CU_TENSOR_MAP_SWIZZLE_32B);
+    if (e != cudaSuccess || !x_bf16) {
+        *x = *x1 = *a;
+        return e;
+    }
+    const cuuint64_t dx[2] = {(cuuint64_t)g.d_in, (cuuint64_t)g.T}, px[1] = {(cuuint64_t)g.ldx * 2};
+    const cuuint32_t bx[2] = {64, (cuuint32_t)rows}, b1[2] = {64, 1};
+    e = make_map(x, g.x, 2, dx, px, bx, CU_TENSOR_MAP_SWIZZLE_128B);
+    return e == cudaSuccess ? make_map(x1, g.x, 2, dx, px, b1, CU_TENSOR_MAP_SWIZZLE_128B) : e;
 }
 
 template <typename XT, int RT>
-static cudaError_t launch_adapter_rt(const AdArgs& g, cudaStream_t s) {
-    if (g.T < 1024) return launch_adapter_t<XT, RT, 16>(g, s);
-    return launch_adapter_t<XT, RT, 64>(g, s);
+static cudaError_t launch_adapter_t(AdArgs g, cudaStream_t s) {
+    using Tile = AdTile<XT, RT>;
+    auto fn = k_adapter<XT, RT>;
+    cudaError_t e = allow_smem((const void*)fn, Tile::SMEM);
+    if (e != cudaSuccess) return e;
+    AdLaunch l;
+    ad_launch(&l, &g, (const void*)fn, Tile::LIST, Tile::WARPS * 32, Tile::SMEM, s);
+    CUtensorMap ma, mb, mx, m1;
+    if ((e = make_maps(g, std::is_same<XT, __nv_bfloat16>::value, Tile::NR, &ma, &mb, &mx, &m1)) != cudaSuccess) return e;
+    return cudaLaunchKernelEx(&l.c, fn, g, ma, mb, mx, m1);
 }
 
 template <typename XT>
-static cudaError_t launch_adapter(const AdArgs& g, cudaStream_t s) {
-    if (g.r_max <= 16) return launch_adapter_rt<XT, 16>(g, s);
-    if (g.r_max <= 32) return launch_adapter_rt<XT, 32>(g, s);
-    if (g.r_max <= 64) return launch_adapter_rt<XT, 64>(g, s);
-    return launch_adapter_rt<XT, 128>(g, s);
+static cudaError_t launch_many(const AdArgs& g, cudaStream_t s) {
+    return g.r_max <= 64 ? launch_adapter_t<XT, 64>(g, s) : launch_adapter_t<XT, 128>(g, s);  // r_max > 32: ad_few
 }
 
 }  // namespace moe
@@ -177,9 +192,10 @@ moe_status moe_adapter(const moe_adapters* ad, void* plan, size_t plan_bytes, co
     g.y = y;
     g.ldy = ldy;
     cudaStream_t s = (cudaStream_t)stream;
-    const cudaError_t e = dtype == MOE_F32    ? launch_adapter<float>(g, s)
-                          : dtype == MOE_BF16 ? launch_adapter<__nv_bfloat16>(g, s)
-                                              : launch_adapter<int8_t>(g, s);
+    const cudaError_t e = ad_few(g) ? launch_adapter_few(g, dtype, s)
+                          : dtype == MOE_F32    ? launch_many<float>(g, s)
+                          : dtype == MOE_BF16 ? launch_many<__nv_bfloat16>(g, s)
+                                              : launch_many<int8_t>(g, s);
     return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, std::string("moe_adapter: ") + cudaGetErrorString(e));
 }
 

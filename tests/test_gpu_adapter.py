@@ -103,6 +103,74 @@ def test_large_shapes(T, n, r_max, d_in, d_out, dtype):
     check(s, T, dtype, owners(T, n, "runs"), base=False)
 
 
+MANY = [  # rows enough for the kernel of many rows (rank above 32, 2048 rows, 256 an adapter)
+    (2048, 1, 40, None, 64, 80), (2111, 3, 64, [64, 33, 0], 272, 528), (2600, 4, 128, [127, 97, 128, 5], 144, 96),
+    (2050, 8, 64, [17, 64, 8, 48, 40, 1, 63, 32], 1040, 272), (4097, 2, 48, [16, 24], 512, 2064)]
+
+
+@pytest.mark.parametrize("T,n,r_max,ranks,d_in,d_out", MANY)
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "i8"])
+def test_many_rows(T, n, r_max, ranks, d_in, d_out, dtype):
+    s = Set(n, r_max, d_in, d_out, ranks)
+    check(s, T, dtype, owners(T, n, "mixed"))
+    check(s, T, dtype, owners(T, n, "runs"), base=False)
+    check(s, T, dtype, owners(T, n, "runs"), in_place=True)
+    check(s, T, dtype, owners(T, n, "one"), ldx=d_in + 48, ldy=d_out + 4)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "i8"])
+@pytest.mark.parametrize("kind", ["mixed", "runs"])
+def test_many_rows_large(dtype, kind):
+    s = Set(4, 64, 6144, 2048, [64, 50, 9, 33])
+    check(s, 3000, dtype, owners(3000, 4, kind))
+    s = Set(2, 64, 1024, 6144, [61, 64])
+    check(s, 2500, dtype, owners(2500, 2, kind))
+
+
+def test_many_rows_in_graphs_and_on_two_streams():
+    s = Set(4, 64, 512, 512, [64, 7, 40, 16])
+    of = owners(2304, 4, "runs")
+    plan = M.adapter_plan(4, of)
+    x, _ = rows(2304, 512, "bf16")
+    y = [torch.empty(2304, 512, device="cuda") for _ in range(3)]
+    M.moe_adapter(s.c, plan, x, y[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    few = M.adapter_plan(4, of[:100].contiguous())
+    z = torch.empty(100, 512, device="cuda")
+    for _ in range(5):  # both kernels at once, too
+        M.moe_adapter(s.c, plan, x, y[1])
+        M.moe_adapter(s.c, plan, x, y[2], stream=side)
+        M.moe_adapter(s.c, few, x[:100], z, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(y[0], y[1]) and torch.equal(y[0], y[2])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        M.moe_adapter_plan(4, of, plan)
+        M.moe_adapter(s.c, plan, x, y[1])
+    of.copy_(owners(2304, 4, "mixed", seed=9))
+    x.copy_(rows(2304, 512, "bf16", seed=10)[0])
+    g.replay()
+    torch.cuda.synchronize()
+    close(y[1], s.want(x, None, of, None))
+
+
+def test_many_rows_that_are_not_finite_stay_alone():
+    s = Set(2, 64, 128, 64)
+    for dtype in ("f32", "bf16"):
+        of = owners(2100, 2, "mixed")
+        of[:4] = torch.tensor([0, 1, 0, -1])
+        x, _ = rows(2100, 128, dtype)
+        clean = x.clone()
+        x[0, 3], x[1, 5], x[3, 0] = float("nan"), float("inf"), float("nan")
+        plan = M.adapter_plan(2, of)
+        y, z = torch.zeros(2100, 64, device="cuda"), torch.zeros(2100, 64, device="cuda")
+        M.moe_adapter(s.c, plan, x, y)
+        M.moe_adapter(s.c, plan, clean, z)
+        assert not torch.isfinite(y[0]).any() and not torch.isfinite(y[1]).any()
+        assert torch.equal(y[2:], z[2:])
+
+
 @pytest.mark.parametrize("dtype,ldx", [("f32", 4), ("f32", 60), ("bf16", 8), ("i8", 16)])
 def test_rows_that_lie_apart(dtype, ldx):
     s = Set(3, 16, 112, 80, [16, 9, 2])
@@ -180,7 +248,7 @@ def test_large_and_tiny_values():
 
 
 def test_plan():
-    """Rows grouped by adapter in their order, tasks of at most 16 and of at most 64."""
+    """Rows grouped by adapter in their order, tasks of at most 8 and of at most 64."""
     for T, n in ((1, 1), (64, 2), (65, 1), (1000, 7), (5000, 300), (3000, 1024), (0, 3)):
         of = owners(T, n, "mixed") if T else torch.empty(0, dtype=torch.int32, device="cuda")
         plan = M.adapter_plan(n, of).cpu()
@@ -191,13 +259,14 @@ def test_plan():
         key[key < 0] = n
         assert order.tolist() == key.sort(stable=True)[1].tolist()
         at = (64 + 4 * T + 15) // 16 * 16
-        for i, most in enumerate((16, 64)):
+        for i, most in enumerate((8, 64)):
             tasks = plan[at:at + 16 * int(head[5 + i])].view(torch.int32).view(-1, 4).tolist()
             at += 16 * (min(T, n + 1) + T // most)
             seen = 0
-            for a, first, cnt, _ in tasks:
+            for a, first, cnt, together in tasks:
                 assert first == seen and 1 <= cnt <= most
                 assert (of.cpu()[order[first:first + cnt].long()] == a).all()
+                assert together == int(bool((order[first:first + cnt].diff() == 1).all()))
                 seen += cnt
             assert seen == T
         assert plan.numel() == at
