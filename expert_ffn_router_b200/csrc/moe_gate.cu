@@ -28,15 +28,39 @@ moe_status check_rule(const moe_config* c, const moe_gate_rule* r) {
     return MOE_OK;
 }
 
-template <typename LT>
+template <typename LT, int NPL, bool VEC>
 static cudaError_t launch_gate_t(const GateArgs& a, cudaStream_t s) {
-    const size_t smem = (size_t)kWarps * a.E * sizeof(double);
-    const void* fn = (const void*)k_gate<LT>;
-    cudaError_t e = allow_smem(fn, smem);
+    const void* fn = (const void*)k_gate<LT, NPL, VEC>;
+    int dev = 0, sms = 148;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    // a warp a row: CTAs of 8 warps, smaller ones while that leaves SMs without any
+    const int warps = std::max(1, std::min(kWarps, a.T / sms));
+    const size_t smem = (size_t)warps * gate_smem(a.E, NPL);
+    const cudaError_t e = allow_smem(fn, (size_t)kWarps * gate_smem(a.E, NPL));
     if (e != cudaSuccess) return e;
-    const int grid = std::min((a.T + kWarps - 1) / kWarps, persistent_grid(fn, smem));
-    k_gate<LT><<<grid, kThreads, smem, s>>>(a);
+    const int grid = std::min((a.T + warps - 1) / warps, persistent_grid(fn, smem, warps * 32));
+    k_gate<LT, NPL, VEC><<<grid, warps * 32, smem, s>>>(a);
     return cudaGetLastError();
+}
+
+template <typename LT, bool VEC>
+static cudaError_t launch_gate_v(const GateArgs& a, cudaStream_t s) {
+    if constexpr (!VEC) {
+        if (a.E <= 32) return launch_gate_t<LT, 1, false>(a, s);
+        if (a.E <= 64) return launch_gate_t<LT, 2, false>(a, s);
+    }
+    if (a.E <= 128) return launch_gate_t<LT, 4, VEC>(a, s);
+    if (a.E <= 256) return launch_gate_t<LT, 8, VEC>(a, s);
+    if (a.E <= 512) return launch_gate_t<LT, 16, VEC>(a, s);
+    return launch_gate_t<LT, 32, VEC>(a, s);
+}
+
+template <typename LT>
+static cudaError_t launch_gate_l(const GateArgs& a, cudaStream_t s) {
+    // four neighbours at a time where every row (and plane) starts on them
+    const bool vec = a.E > 64 && a.E % 4 == 0 && a.ld % 4 == 0 && a.plane % 4 == 0;
+    return vec ? launch_gate_v<LT, true>(a, s) : launch_gate_v<LT, false>(a, s);
 }
 
 cudaError_t launch_gate(const moe_config* c, const moe_gate_rule* r, const void* logits, moe_dtype dt, long long ld,
@@ -61,7 +85,7 @@ cudaError_t launch_gate(const moe_config* c, const moe_gate_rule* r, const void*
     a.topp = c->topp;
     a.idx = idx;
     a.w = w;
-    return dt == MOE_BF16 ? launch_gate_t<__nv_bfloat16>(a, s) : launch_gate_t<float>(a, s);
+    return dt == MOE_BF16 ? launch_gate_l<__nv_bfloat16>(a, s) : launch_gate_l<float>(a, s);
 }
 
 }  // namespace moe
