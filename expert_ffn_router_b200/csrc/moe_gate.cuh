@@ -34,6 +34,21 @@ __device__ __forceinline__ float gate_logit(const GateArgs& a, int t, int e) {
     return v;
 }
 
+// The largest of a warp's floats (none of them NaN).
+__device__ __forceinline__ float gate_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+// 1 / (1 + exp(-l)) within 3e-7 of it: 2^x within 2^-22, by s (1 - s) <= 1/4;
+// the sum 2^-24; the reciprocal 2^-23.
+__device__ __forceinline__ float gate_sigmoid(float l) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(l * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
+}
+
 __device__ __forceinline__ double warp_sum_f64(double v) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
@@ -222,8 +237,8 @@ __host__ __device__ constexpr int gate_smem(int E, int npl) {
 }
 
 // Which groups stay: bit g L of the result for group g, whose values lie at
-// v[g (gs + L)] on.  lo, hi: the smallest value of those that stay, the largest
-// of the others.
+// v[g (gs + L)] on.  lo, hi (float only): the smallest value of those that stay,
+// the largest of the others.
 template <typename T>
 __device__ __forceinline__ unsigned gate_groups(const GateArgs& a, int L, const T* v, T& lo, T& hi) {
     const int lane = threadIdx.x & 31, g = lane / L, sub = lane % L;
@@ -232,7 +247,10 @@ __device__ __forceinline__ unsigned gate_groups(const GateArgs& a, int L, const 
     if (g < a.G)
         for (int i = sub; i < a.gs; i += L) {
             const T x = v[g * (a.gs + L) + i];
-            if (x > v1) {
+            if constexpr (sizeof(T) == 4) {
+                v2 = fmaxf(v2, fminf(v1, x));
+                v1 = fmaxf(v1, x);
+            } else if (x > v1) {
                 v2 = v1;
                 v1 = x;
             } else if (x > v2) {
@@ -252,12 +270,9 @@ __device__ __forceinline__ unsigned gate_groups(const GateArgs& a, int L, const 
         better += x > gv || (x == gv && j < g);
     }
     const bool in = g < a.G && gv > none && better < a.keep;
-    lo = in ? gv : (T)INFINITY;
-    hi = g < a.G && !in ? gv : none;
-    for (int o = 16; o; o >>= 1) {
-        const T x = __shfl_xor_sync(kFull, lo, o), y = __shfl_xor_sync(kFull, hi, o);
-        lo = x < lo ? x : lo;
-        hi = y > hi ? y : hi;
+    if constexpr (sizeof(T) == 4) {
+        lo = -gate_max(in ? -gv : none);
+        hi = gate_max(g < a.G && !in ? gv : none);
     }
     return __ballot_sync(kFull, in);
 }
@@ -333,14 +348,19 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
     int L = 1;
     while (L * 2 * G <= 32) L *= 2;
     float b[NPL];
-    int pos[NPL];  // place in shared memory; its group's first lane in the top byte
+    int pos[NPL];      // place among the groups' values in shared memory
+    unsigned gbit[NPL];  // its group's bit, 0 behind the last expert
+    bool b_out = false;
 #pragma unroll
     for (int i = 0; i < NPL; ++i) {
         const int e = i / V * 32 * V + lane * V + i % V;
         b[i] = a.bias && e < a.E ? fmaxf(__ldg(a.bias + e), -INFINITY) : 0.0f;  // NaN: -inf
         const int g = G > 1 && e < a.E ? e / a.gs : 0;
-        pos[i] = (e + g * L) | (g * L) << 24;
+        pos[i] = e + g * L;
+        gbit[i] = e < a.E ? 1u << (g * L) : 0u;
+        b_out |= b[i] == -INFINITY;
     }
+    b_out = __any_sync(kFull, b_out);
     for (long long t0 = (long long)blockIdx.x * warps + warp; t0 < a.T; t0 += (long long)gridDim.x * warps) {
         const int t = (int)t0;
         float l[NPL], v[NPL];
@@ -349,12 +369,13 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
             l[i] = fmaxf(l[i], -INFINITY);  // NaN: -inf
-            if (b[i] == -INFINITY) l[i] = -INFINITY;
-            m = fmaxf(m, l[i]);
+            if (b_out && b[i] == -INFINITY) l[i] = -INFINITY;
         }
         bool redo = false;
         if (a.softmax) {
-            m = warp_max(m);
+#pragma unroll
+            for (int i = 0; i < NPL; ++i) m = fmaxf(m, l[i]);
+            m = gate_max(m);
             redo = m == INFINITY;
         }
         if (a.softmax && (a.bias || a.raw || G > 1)) {
@@ -373,8 +394,8 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
             eps = 4e-6f * rz;  // of the largest score: exponential and sum, 32 roundings of 2^-23
         } else if (!a.softmax && (a.bias || G > 1)) {
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) v[i] = __fdividef(1.0f, 1.0f + __expf(-l[i]));
-            eps = 5e-7f;  // exponential 7e-8 (its 2 + 1.2 |l| ulp by s (1 - s)), sum 6e-8, quotient 2.4e-7
+            for (int i = 0; i < NPL; ++i) v[i] = gate_sigmoid(l[i]);
+            eps = 4e-7f;
         }
         // selection values (and the scores plus bias that groups count by)
         float top = -INFINITY, bot = INFINITY, widest = 0.0f;
@@ -383,8 +404,7 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
             if (a.bias) v[i] += b[i];
             if (G > 1) widest = fmaxf(widest, l[i] > -INFINITY ? fabsf(v[i]) : 0.0f);
             if (G > 1) {
-                const int e = i / V * 32 * V + lane * V + i % V;
-                if (e < a.E) fs[pos[i] & 0xffffff] = l[i] > -INFINITY ? v[i] : -INFINITY;
+                if (gbit[i]) fs[pos[i]] = l[i] > -INFINITY ? v[i] : -INFINITY;
             }
         }
         unsigned stay = kFull;
@@ -394,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
             stay = gate_groups<float>(a, L, fs, lo, hi);
             __syncwarp();
             // two sums of two values each, six roundings of at most 2^-24 of twice the widest value
-            if (hi > -INFINITY && !(lo - hi > 4.0f * eps + 1e-6f * warp_max(widest)) && !redo)
+            if (hi > -INFINITY && !(lo - hi > 4.0f * eps + 1e-6f * gate_max(widest)) && !redo)
                 stay = gate_groups_f64<LT>(a, t, m, L, sel);
         }
         if (!a.bias) {  // by the logits themselves, which are exact
@@ -405,13 +425,13 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
         unsigned key[NPL];
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            const bool in = l[i] > -INFINITY && (G == 1 || (stay >> (pos[i] >> 24)) & 1u);
+            const bool in = l[i] > -INFINITY && (stay & gbit[i]);
             key[i] = in;
             top = fmaxf(top, in ? v[i] : -INFINITY);
             bot = fminf(bot, in ? v[i] : INFINITY);
         }
-        top = warp_max(top);
-        bot = -warp_max(-bot);
+        top = gate_max(top);
+        bot = -gate_max(-bot);
         const float range = top - bot;
         redo |= top > bot && !(range < 1e37f);  // infinite, or nearly
         const float inv = range > 0.0f && range < 1e37f ? 0.9999990f / range : 0.0f;
@@ -434,20 +454,18 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
         }
         int at = 1, c = 0;  // c: candidates, the i-th in lane i's `mine`, the 32 + i-th in its `mine2`
         auto give = [&](unsigned mx) {
-            if (lane == c) mine = mx;
-            if (lane + 32 == c) mine2 = mx;
-            ++c;
-            kth = mx;
             if (head == mx) {
                 head = NPL > 1 && at < NPL ? us[at * 32 + lane] : 0u;
                 ++at;
             }
         };
-        unsigned mx = 0u;
-        for (int j = 0; j <= k; ++j) {
-            mx = __reduce_max_sync(kFull, head);
-            if (mx == 0u || j == k) break;
+        unsigned mx = __reduce_max_sync(kFull, head);
+        while (c < k && mx) {
+            if (lane == c) mine = mx;
             give(mx);
+            ++c;
+            kth = mx;
+            mx = __reduce_max_sync(kFull, head);
         }
         int e_mine = mine ? (int)(IM - (mine & IM)) : -1;
         float l_mine = e_mine >= 0 ? gate_logit<LT>(a, t, e_mine) : 0.0f;
@@ -469,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
                 if (G > 1 && !((stay >> (e / a.gs * L)) & 1u)) continue;
                 const float ve = !a.bias     ? le
                                  : a.softmax ? (a.raw ? expf(le - m) : __expf(le - m)) * __frcp_rn(z) + be
-                                             : __fdividef(1.0f, 1.0f + __expf(-le)) + be;
+                                             : gate_sigmoid(le) + be;
                 const unsigned f = (__float_as_uint(fmaf(ve - bot, inv, 1.0f)) & 0x7fffffu) >> (23 - VB);
                 const unsigned ke = 0x80000000u | f << IB | (IM - (unsigned)e);
                 more = ke < last && (last >> IB) - (ke >> IB) <= tol + 2;
@@ -481,7 +499,10 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
                         redo = true;  // more candidates than two a lane
                         break;
                     }
+                    if (lane == c) mine = mx;
+                    if (lane + 32 == c) mine2 = mx;
                     give(mx);
+                    ++c;
                     mx = __reduce_max_sync(kFull, head);
                 }
                 e_mine = mine ? (int)(IM - (mine & IM)) : -1;
