@@ -329,15 +329,32 @@ def gate_rule(score: str = "sigmoid", n_groups: int = 0, topk_groups: int = 0, g
                        {"top2": MOE_GROUP_TOP2, "max": MOE_GROUP_MAX}[group_value], 0 if renorm else 1)
 
 
-def _rows(t: torch.Tensor, d: int, name: str, dtype=None):
-    """Pointer and row stride of a [T][d] matrix whose rows may lie apart."""
+def _here(t: torch.Tensor, name: str) -> int:
+    """The current device, which ``t`` must be on."""
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name}: expected a tensor on the current device")
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on the current device, cuda:{dev}, got {t.device}")
+    return dev
+
+
+def _arg(t: torch.Tensor, dev: int, dtype, numel: int, name: str) -> int:
+    """_ptr for a tensor on the current device (its checks in one expression:
+    a call of the small operators is shorter than their host time)."""
+    if t.get_device() != dev or t.dtype is not dtype or t.numel() != numel or not t.is_contiguous():
+        _ptr(t, dtype, numel, name)
+        raise ValueError(f"{name}: expected a tensor on the current device, cuda:{dev}, got {t.device}")
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, dev: int, d: int, name: str, dtype=None):
+    """Pointer and row stride of a [T][d] matrix whose rows may lie apart."""
+    if t.get_device() != dev:
+        _here(t, name)
     if t.dim() != 2 or t.shape[1] != d:
         raise ValueError(f"{name}: expected [T][{d}], got {list(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     ld, step = t.stride()
     if step != 1 and d > 1:
@@ -345,16 +362,26 @@ def _rows(t: torch.Tensor, d: int, name: str, dtype=None):
     return t.data_ptr(), ld if t.shape[0] > 1 else max(ld, d)
 
 
+def _stream_on(stream: Optional[torch.cuda.Stream], dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+_DTYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.int8: MOE_I8}
+
+
 def moe_gate(cfg: MoeConfig, rule: MoeGateRule, logits: torch.Tensor, bias: Optional[torch.Tensor],
              topk_idx: torch.Tensor, topk_w: torch.Tensor, stream=None):
     """Selects experts from logits [T][E] (float32 or bfloat16; rows may be a
     slice of a wider matrix): indices (-1: no expert) and weights."""
-    T = logits.shape[0]
-    p, ld = _rows(logits, cfg.n_experts, "logits")
-    _check(lib.moe_gate(ctypes.byref(cfg), ctypes.byref(rule), p, _xdtype(logits), ld, T,
-                        _ptr(bias, torch.float32, cfg.n_experts, "bias"),
-                        _ptr(topk_idx, torch.int32, T * cfg.top_k, "topk_idx"),
-                        _ptr(topk_w, torch.float32, T * cfg.top_k, "topk_w"), _stream(stream)), "moe_gate")
+    dev = _here(logits, "logits")
+    p, ld = _rows(logits, dev, cfg.n_experts, "logits")
+    T, k = logits.shape[0], cfg.top_k
+    st = lib.moe_gate(ctypes.byref(cfg), ctypes.byref(rule), p, _xdtype(logits), ld, T,
+                      None if bias is None else _arg(bias, dev, torch.float32, cfg.n_experts, "bias"),
+                      _arg(topk_idx, dev, torch.int32, T * k, "topk_idx"),
+                      _arg(topk_w, dev, torch.float32, T * k, "topk_w"), _stream_on(stream, dev))
+    if st != MOE_OK:
+        _check(st, "moe_gate")
 
 
 def moe_route_gated(cfg: MoeConfig, rule: MoeGateRule, x: torch.Tensor, w_router: torch.Tensor,
@@ -422,15 +449,21 @@ def moe_adapter(ad: MoeAdapters, plan: torch.Tensor, x: torch.Tensor, y: torch.T
                 base: Optional[torch.Tensor] = None, sx: Optional[torch.Tensor] = None, stream=None):
     """y = base + the rows' adapters of x (float32, bfloat16, or int8 codes
     with ``sx``); ``base`` may be ``y``; rows may lie apart."""
+    dev = _here(x, "x")
     T = x.shape[0]
-    xp, ldx = _rows(x, ad.d_in, "x")
-    yp, ldy = _rows(y, ad.d_out, "y", torch.float32)
-    bp, ldb = _rows(base, ad.d_out, "base", torch.float32) if base is not None else (None, 0)
+    xp, ldx = _rows(x, dev, ad.d_in, "x")
+    yp, ldy = _rows(y, dev, ad.d_out, "y", torch.float32)
+    bp, ldb = _rows(base, dev, ad.d_out, "base", torch.float32) if base is not None else (None, 0)
     if y.shape[0] != T or (base is not None and base.shape[0] != T):
         raise ValueError(f"x, y and base: expected {T} rows each")
-    _check(lib.moe_adapter(ctypes.byref(ad), _ptr(plan, torch.uint8, name="plan"), plan.numel(), xp,
-                           MOE_I8 if x.dtype == torch.int8 else _xdtype(x), _ptr(sx, torch.float32, T, "sx"), ldx, T,
-                           bp, ldb, yp, ldy, _stream(stream)), "moe_adapter")
+    if x.dtype not in _DTYPES:
+        raise ValueError(f"x must be float32, bfloat16 or int8, got {x.dtype}")
+    n = plan.numel()
+    st = lib.moe_adapter(ctypes.byref(ad), _arg(plan, dev, torch.uint8, n, "plan"), n, xp, _DTYPES[x.dtype],
+                         None if sx is None else _arg(sx, dev, torch.float32, T, "sx"), ldx, T, bp, ldb, yp, ldy,
+                         _stream_on(stream, dev))
+    if st != MOE_OK:
+        _check(st, "moe_adapter")
 
 
 def moe_rmsnorm(x: torch.Tensor, x_in: torch.Tensor, eps: float = 1e-6, x_copy=None, stream=None):
