@@ -359,7 +359,7 @@ def _rows(t: torch.Tensor, dev: int, d: int, name: str, dtype=None):
     ld, step = t.stride()
     if step != 1 and d > 1:
         raise ValueError(f"{name}: expected rows of neighbouring elements")
-    return t.data_ptr(), ld if t.shape[0] > 1 else max(ld, d)
+    return t.data_ptr(), ld if t.shape[0] > 1 else d  # one row's distance to the next says nothing
 
 
 def _stream_on(stream: Optional[torch.cuda.Stream], dev: int) -> int:

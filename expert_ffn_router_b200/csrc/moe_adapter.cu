@@ -68,8 +68,8 @@ static cudaError_t make_map(CUtensorMap* tm, const void* p, int rank, const cuui
 }
 
 // A: rows of components, 64 columns x 16 rows a box.  B: outputs in pairs, 16
-// components x 128 outputs of one parity a box.  x (bf16): 64
-// columns of `rows` neighbouring rows, and of one.
+// components x 128 outputs of one parity a box.  x (bf16): 64 columns of `rows`
+// neighbouring rows, and of one.
 static cudaError_t make_maps(const AdArgs& g, bool x_bf16, int rows, CUtensorMap* a, CUtensorMap* b, CUtensorMap* x,
                              CUtensorMap* x1) {
     const cuuint64_t da[2] = {(cuuint64_t)g.d_in, (cuuint64_t)g.n * g.r_max}, pa[1] = {(cuuint64_t)g.d_in * 2};
@@ -114,16 +114,18 @@ using namespace moe;
 
 extern "C" {
 
-size_t moe_adapter_plan_bytes(int32_t n_adapters, int32_t max_tokens) {
+size_t moe_adapter_plan_bytes(int32_t n_adapters, int32_t max_tokens) try {
     if (n_adapters < 1 || n_adapters > kAdMaxN || max_tokens < 0) {
         fail(MOE_EINVAL, "n_adapters must be in [1, 1024] and max_tokens >= 0");
         return 0;
     }
     return ad_plan_carve(nullptr, n_adapters, max_tokens).bytes;
+} catch (...) {  // (out of host memory)
+    return 0;
 }
 
 moe_status moe_adapter_plan(int32_t n_adapters, const int32_t* adapter_of, int32_t T, void* plan, size_t plan_bytes,
-                            moe_stream_t stream) {
+                            moe_stream_t stream) try {
     moe_status st = check_plan_args(n_adapters, T, plan, plan_bytes);
     if (st != MOE_OK) return st;
     if (T > 0 && (st = check_ptr(adapter_of, "adapter_of")) != MOE_OK) return st;
@@ -135,11 +137,13 @@ moe_status moe_adapter_plan(int32_t n_adapters, const int32_t* adapter_of, int32
         e = cudaGetLastError();
     }
     return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, std::string("moe_adapter_plan: ") + cudaGetErrorString(e));
+} catch (...) {
+    return MOE_ECUDA;
 }
 
 moe_status moe_adapter(const moe_adapters* ad, void* plan, size_t plan_bytes, const void* x, moe_dtype dtype,
                        const float* sx, int64_t ldx, int32_t T, const float* base, int64_t ldbase, float* y,
-                       int64_t ldy, moe_stream_t stream) {
+                       int64_t ldy, moe_stream_t stream) try {
     moe_status st;
     if (!ad) return fail(MOE_EINVAL, "ad is NULL");
     if (ad->r_max < 8 || ad->r_max > kAdMaxRank || ad->r_max % 8)
@@ -197,6 +201,8 @@ moe_status moe_adapter(const moe_adapters* ad, void* plan, size_t plan_bytes, co
                           : dtype == MOE_BF16 ? launch_many<__nv_bfloat16>(g, s)
                                               : launch_many<int8_t>(g, s);
     return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, std::string("moe_adapter: ") + cudaGetErrorString(e));
+} catch (...) {
+    return MOE_ECUDA;
 }
 
 }  // extern "C"

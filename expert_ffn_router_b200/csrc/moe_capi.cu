@@ -636,7 +636,7 @@ moe_status moe_layer(const moe_config* cfg, const moe_pool* pool, const float* w
 
 moe_status moe_route_gated(const moe_config* cfg, const moe_gate_rule* rule, const void* x, moe_dtype dtype, int32_t T,
                            const float* w_router, const float* bias, int32_t* topk_idx, float* topk_w, void* ws,
-                           size_t ws_bytes, moe_stream_t stream) {
+                           size_t ws_bytes, moe_stream_t stream) try {
     MOE_TRY(check_cfg(cfg));
     MOE_TRY(check_rule(cfg, rule));
     MOE_TRY(check_dtype(dtype));
@@ -657,11 +657,13 @@ moe_status moe_route_gated(const moe_config* cfg, const moe_gate_rule* rule, con
         e = launch_gate(cfg, rule, p.ws.logits, MOE_F32, cfg->n_experts, p.ksplit, (long long)T * cfg->n_experts, T,
                         bias, topk_idx, topk_w, s);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_route_gated");
+} catch (...) {  // (out of host memory)
+    return MOE_ECUDA;
 }
 
 moe_status moe_layer_routed(const moe_config* cfg, const moe_pool* pool, const int32_t* topk_idx, const float* topk_w,
                             const void* x, moe_dtype dtype, int32_t T, float* out, int32_t accumulate, void* ws,
-                            size_t ws_bytes, moe_stream_t stream) {
+                            size_t ws_bytes, moe_stream_t stream) try {
     MOE_TRY(check_cfg(cfg));
     MOE_TRY(check_dtype(dtype));
     if (!pool) return fail(MOE_EINVAL, "pool is NULL");
@@ -723,6 +725,8 @@ moe_status moe_layer_routed(const moe_config* cfg, const moe_pool* pool, const i
     if (e == cudaSuccess) e = launch_gate_up(p, tl, false, s);
     if (e == cudaSuccess) e = launch_down(p, tl, false, s);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "moe_layer_routed");
+} catch (...) {  // (out of host memory)
+    return MOE_ECUDA;
 }
 
 moe_status moe_rmsnorm(const void* x, moe_dtype dtype, int32_t T, int32_t d, float eps, float* x_in, float* x_copy,

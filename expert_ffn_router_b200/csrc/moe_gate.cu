@@ -94,7 +94,7 @@ using namespace moe;
 
 extern "C" moe_status moe_gate(const moe_config* cfg, const moe_gate_rule* rule, const void* logits, moe_dtype dtype,
                                int64_t ld, int32_t T, const float* bias, int32_t* topk_idx, float* topk_w,
-                               moe_stream_t stream) {
+                               moe_stream_t stream) try {
     moe_status st = check_cfg(cfg);
     if (st != MOE_OK) return st;
     if ((st = check_rule(cfg, rule)) != MOE_OK) return st;
@@ -109,4 +109,6 @@ extern "C" moe_status moe_gate(const moe_config* cfg, const moe_gate_rule* rule,
     const cudaError_t e = launch_gate(cfg, rule, logits, dtype, ld, 1, 0, T, bias, topk_idx, topk_w,
                                       (cudaStream_t)stream);
     return e == cudaSuccess ? MOE_OK : fail(MOE_ECUDA, std::string("moe_gate: ") + cudaGetErrorString(e));
+} catch (...) {  // (out of host memory)
+    return MOE_ECUDA;
 }

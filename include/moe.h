@@ -370,7 +370,8 @@ typedef struct {
 /* Bytes of the plan of up to max_tokens rows (0: an argument out of range). */
 MOE_API size_t moe_adapter_plan_bytes(int32_t n_adapters, int32_t max_tokens);
 
-/* adapter_of int32 [T] (device; -1: no adapter) -> plan.  An entry outside
+/* adapter_of int32 [T] (device; -1: no adapter) -> plan.  A plan that is made
+ * anew must not be in use by another stream's call.  An entry outside
  * [-1, n_adapters) is recorded as MOE_EDEVICE in the plan's status word
  * (moe_poll_status(plan, ...)) and counts as -1.  The order of the rows of an
  * adapter is theirs in the batch. */
@@ -381,7 +382,8 @@ MOE_API moe_status moe_adapter_plan(int32_t n_adapters, const int32_t* adapter_o
  * sx), rows ldx elements apart (16-byte aligned rows); base and y fp32
  * [T][d_out], rows ldbase and ldy elements apart (multiples of 4).  base NULL:
  * y[t] = the update alone (0 without an adapter).  base may be y (in place,
- * with ldbase = ldy); otherwise y must overlap none of the inputs.  T must be
+ * with ldbase = ldy); otherwise y must overlap none of the inputs (from
+ * the first row's start to the last one's end).  T must be
  * the plan's, n_adapters too: a mismatch is recorded as MOE_EDEVICE in the
  * plan's status word and nothing is written.  No workspace: calls on one plan
  * may overlap.  Rows from T on are left as they are. */
