@@ -233,7 +233,7 @@ __device__ __forceinline__ void gate_load_row(const GateArgs& a, int t, float (&
 // Shared memory of a warp: E doubles and 32 for the groups' distance (before and
 // after that float32 values and sorted keys in the same place).
 __host__ __device__ constexpr int gate_smem(int E, int npl) {
-    return ((E + 32) * 8 > npl * 128 ? (E + 32) * 8 : npl * 128) / 16 * 16 + 16;
+    return ((E + 32) * 8 > npl * 128 + 128 ? (E + 32) * 8 : npl * 128 + 128) / 16 * 16 + 16;
 }
 
 // Which groups stay: bit g L of the result for group g, whose values lie at
@@ -245,6 +245,7 @@ __device__ __forceinline__ unsigned gate_groups(const GateArgs& a, int L, const 
     const T none = -INFINITY;
     T v1 = none, v2 = none;
     if (g < a.G)
+#pragma unroll 4
         for (int i = sub; i < a.gs; i += L) {
             const T x = v[g * (a.gs + L) + i];
             if constexpr (sizeof(T) == 4) {
@@ -265,6 +266,7 @@ __device__ __forceinline__ unsigned gate_groups(const GateArgs& a, int L, const 
     }
     const T gv = !a.gmax && v2 > none ? v1 + v2 : v1;
     int better = 0;
+#pragma unroll 4
     for (int j = 0; j < a.G; ++j) {
         const T x = __shfl_sync(kFull, gv, j * L);
         better += x > gv || (x == gv && j < g);
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
         const int e = i / V * 32 * V + lane * V + i % V;
         b[i] = a.bias && e < a.E ? fmaxf(__ldg(a.bias + e), -INFINITY) : 0.0f;  // NaN: -inf
         const int g = G > 1 && e < a.E ? e / a.gs : 0;
-        pos[i] = e + g * L;
+        pos[i] = e < a.E ? e + g * L : a.E + 32;  // (a place that nobody reads)
         gbit[i] = e < a.E ? 1u << (g * L) : 0u;
         b_out |= b[i] == -INFINITY;
     }
@@ -404,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
             if (a.bias) v[i] += b[i];
             if (G > 1) widest = fmaxf(widest, l[i] > -INFINITY ? fabsf(v[i]) : 0.0f);
             if (G > 1) {
-                if (gbit[i]) fs[pos[i]] = l[i] > -INFINITY ? v[i] : -INFINITY;
+                fs[pos[i]] = l[i] > -INFINITY ? v[i] : -INFINITY;
             }
         }
         unsigned stay = kFull;
@@ -446,27 +448,32 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
             key[i] = key[i] ? 0x80000000u | (f >> (23 - VB)) << IB | (IM - (unsigned)e) : 0u;
         }
         if (NPL > 1) gate_sort<NPL>(key);
-        unsigned head = key[0], mine = 0u, mine2 = 0u, kth = 0u;
+        // the lane's keys one by one: head, then next, read ahead; zeros behind the last
+        unsigned head = key[0], mine = 0u, mine2 = 0u;
         if (NPL > 1) {
 #pragma unroll
             for (int i = 1; i < NPL; ++i) us[i * 32 + lane] = key[i];
-            __syncwarp();
         }
-        int at = 1, c = 0;  // c: candidates, the i-th in lane i's `mine`, the 32 + i-th in its `mine2`
+        us[NPL * 32 + lane] = 0u;
+        const unsigned* next_at = us + 32 + lane;
+        unsigned next = NPL > 1 ? key[NPL > 1 ? 1 : 0] : 0u;
+        __syncwarp();
         auto give = [&](unsigned mx) {
-            if (head == mx) {
-                head = NPL > 1 && at < NPL ? us[at * 32 + lane] : 0u;
-                ++at;
-            }
+            const bool own = head == mx;
+            head = own ? next : head;
+            next_at += own && next ? 32 : 0;
+            next = *next_at;
         };
         unsigned mx = __reduce_max_sync(kFull, head);
-        while (c < k && mx) {
-            if (lane == c) mine = mx;
+#pragma unroll 2
+        for (int j = 0; j < k; ++j) {  // (zeros, once no expert is left)
+            mine = lane == j ? mx : mine;
             give(mx);
-            ++c;
-            kth = mx;
             mx = __reduce_max_sync(kFull, head);
         }
+        // candidates: the i-th in lane i's `mine`, the 32 + i-th in its `mine2`
+        int c = __popc(__ballot_sync(kFull, mine != 0u));
+        const unsigned kth = __shfl_sync(kFull, mine, k - 1);
         int e_mine = mine ? (int)(IM - (mine & IM)) : -1;
         float l_mine = e_mine >= 0 ? gate_logit<LT>(a, t, e_mine) : 0.0f;
         const float b_mine = a.bias && e_mine >= 0 ? __ldg(a.bias + e_mine) : 0.0f;
