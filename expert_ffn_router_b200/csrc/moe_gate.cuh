@@ -175,6 +175,12 @@ static __device__ __noinline__ void gate_row_f64(const GateArgs& a, int t, doubl
 //
 // Lane l holds the experts (i / V) * 32 V + l V + i % V, V = min(NPL, 4), so
 // that it reads 16 (bf16: 8) bytes at a time where rows allow it (VEC).
+//
+// Bound by the instructions a row takes, not by its bytes: 1090 for 256 experts
+// in 8 groups, 8 selected (ncu, 66% of the issue slots): 65536 such rows in
+// 100 us, 0.71 TB/s against 6.55 of a copy, where every row in double precision
+// took 426.  1024 experts, 32 selected: 4096 rows in 37 us (double 107).  One
+// row: 4.0 us, the launch and a chain of some thirty dependent steps.
 // ---------------------------------------------------------------------------
 // Descending: odd-even merge sort, the places known to the compiler.
 template <int N, int P, int K>
