@@ -388,6 +388,7 @@ def moe_route_gated(cfg: MoeConfig, rule: MoeGateRule, x: torch.Tensor, w_router
                     bias: Optional[torch.Tensor], topk_idx: torch.Tensor, topk_w: torch.Tensor, ws: torch.Tensor,
                     stream=None):
     """moe_route with the selection of moe_gate."""
+    _here(x, "x")
     T = x.shape[0]
     _check(lib.moe_route_gated(ctypes.byref(cfg), ctypes.byref(rule), _ptr(x, None, T * cfg.d, "x"), _xdtype(x), T,
                                _ptr(w_router, torch.float32, cfg.n_experts * cfg.d, "w_router"),
@@ -400,6 +401,7 @@ def moe_route_gated(cfg: MoeConfig, rule: MoeGateRule, x: torch.Tensor, w_router
 def moe_layer_routed(cfg: MoeConfig, pool: MoePool, topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
                      out: torch.Tensor, ws: torch.Tensor, accumulate: bool = False, stream=None):
     """moe_layer for a routing the caller has."""
+    _here(x, "x")
     T = x.shape[0]
     _check(lib.moe_layer_routed(ctypes.byref(cfg), ctypes.byref(pool),
                                 _ptr(topk_idx, torch.int32, T * cfg.top_k, "topk_idx"),
@@ -432,6 +434,9 @@ def moe_adapter_plan_bytes(n_adapters: int, max_tokens: int) -> int:
 
 
 def moe_adapter_plan(n_adapters: int, adapter_of: torch.Tensor, plan: torch.Tensor, stream=None):
+    """The plan of a batch whose row t has the adapter ``adapter_of[t]`` (int32,
+    -1: none), into ``plan``."""
+    _here(adapter_of, "adapter_of")
     _check(lib.moe_adapter_plan(n_adapters, _ptr(adapter_of, torch.int32, name="adapter_of"), adapter_of.numel(),
                                 _ptr(plan, torch.uint8, name="plan"), plan.numel(), _stream(stream)),
            "moe_adapter_plan")
