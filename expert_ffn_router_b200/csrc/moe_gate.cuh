@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
             z = warp_sum(e_sum);
             const float rz = __frcp_rn(z);
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) v[i] *= rz;
+            for (int i = 0; i < NPL; ++i) v[i] = __fmul_rn(v[i], rz);  // (not fused: the border's search has it again)
             eps = 4e-6f * rz;  // of the largest score: exponential and sum, 32 roundings of 2^-23
         } else if (!a.softmax && (a.bias || G > 1)) {
 #pragma unroll
@@ -409,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
         float top = -INFINITY, bot = INFINITY, widest = 0.0f;
 #pragma unroll
         for (int i = 0; i < NPL; ++i) {
-            if (a.bias) v[i] += b[i];
+            if (a.bias) v[i] = __fadd_rn(v[i], b[i]);
             if (G > 1) widest = fmaxf(widest, l[i] > -INFINITY ? fabsf(v[i]) : 0.0f);
             if (G > 1) {
                 fs[pos[i]] = l[i] > -INFINITY ? v[i] : -INFINITY;
@@ -489,23 +489,26 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
         bool unsure = __any_sync(kFull, lane < c - 1 && (mine >> IB) - (near >> IB) <= tol &&
                                             !(l_mine == l_nx && b_mine == b_nx));
         if (c == k && mx && (kth >> IB) - (mx >> IB) <= tol) {
-            // others may belong to the k: those as near to the last of them that are not its equals (or that
-            // are, if the order of the k is not sure)
+            // others may belong to the k: those not clearly below the last of them that are not its equals (or that
+            // are, if the order of the k is not sure).  All experts above that line are counted, their values computed
+            // again, operation by operation; more than stand among the k, and the others are to be compared.
             const float l_k = __shfl_sync(kFull, l_mine, k - 1), b_k = __shfl_sync(kFull, b_mine, k - 1);
             const unsigned last = kth;
-            bool more = unsure;
-            for (int e = lane; e < a.E && !more; e += 32) {
+            int above = 0;
+#pragma unroll 1
+            for (int e = lane; e < a.E && !unsure; e += 32) {
                 const float le = fmaxf(gate_logit<LT>(a, t, e), -INFINITY), be = a.bias ? __ldg(a.bias + e) : 0.0f;
                 if (!(le > -INFINITY && be > -INFINITY) || (le == l_k && be == b_k)) continue;
                 if (G > 1 && !((stay >> (e / a.gs * L)) & 1u)) continue;
-                const float ve = !a.bias     ? le
-                                 : a.softmax ? (a.raw ? expf(le - m) : __expf(le - m)) * __frcp_rn(z) + be
-                                             : gate_sigmoid(le) + be;
+                float ve = le;
+                if (a.bias)
+                    ve = __fadd_rn(a.softmax ? __fmul_rn(a.raw ? expf(le - m) : __expf(le - m), __frcp_rn(z))
+                                             : gate_sigmoid(le), be);
                 const unsigned f = (__float_as_uint(fmaf(ve - bot, inv, 1.0f)) & 0x7fffffu) >> (23 - VB);
-                const unsigned ke = 0x80000000u | f << IB | (IM - (unsigned)e);
-                more = ke < last && (last >> IB) - (ke >> IB) <= tol + 2;
+                above += (0x80000000u >> IB | f) + tol + 2u >= last >> IB;
             }
-            if (__any_sync(kFull, more)) {
+            const int among = __popc(__ballot_sync(kFull, lane < k && !(l_mine == l_k && b_mine == b_k)));
+            if (unsure || __reduce_add_sync(kFull, above) > among) {
                 unsure = true;
                 while (mx && (last >> IB) - (mx >> IB) <= tol) {
                     if (c == 64) {
