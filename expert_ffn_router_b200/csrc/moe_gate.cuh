@@ -421,8 +421,10 @@ __global__ void __launch_bounds__(kThreads, NPL <= 4 ? 4 : NPL == 8 ? 3 : 2) k_g
             float lo, hi;
             stay = gate_groups<float>(a, L, fs, lo, hi);
             __syncwarp();
+            widest = gate_max(widest);
+            redo |= !(widest < 1e37f);  // a sum of two might leave float32
             // two sums of two values each, six roundings of at most 2^-24 of twice the widest value
-            if (hi > -INFINITY && !(lo - hi > 4.0f * eps + 1e-6f * gate_max(widest)) && !redo)
+            if (hi > -INFINITY && !(lo - hi > 4.0f * eps + 1e-6f * widest) && !redo)
                 stay = gate_groups_f64<LT>(a, t, m, L, sel);
         }
         if (!a.bias) {  // by the logits themselves, which are exact

@@ -1,9 +1,12 @@
 """moe_gate where the border between the selected and the others is as narrow
-as the types allow: the order is the double-precision one."""
+as the types allow, or where sums leave float32's range: the order is the
+double-precision one."""
+import numpy as np
 import pytest
 import torch
 
 import expert_ffn_router_b200 as M
+from gate_reference import gate
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +64,35 @@ def test_borders_within_a_float32_rounding(E, k, score, renorm):
     want = torch.sort(v, dim=1, descending=True, stable=True)[1][:, :k].to(torch.int32)
     wrong = (idx != want).any(1)
     assert not wrong.any(), f"{int(wrong.sum())} of {T} rows"
+
+
+LOW = torch.finfo(torch.float32).min
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("value", ["top2", "max"])
+@pytest.mark.parametrize("E,G,keep,k", [(24, 3, 2, 5), (64, 8, 3, 8), (256, 8, 4, 8), (1024, 32, 3, 32)])
+def test_groups_whose_sums_leave_float32(score, value, E, G, keep, k):
+    """Biases of the type's lowest value (a mask, to some callers) are values
+    like others: the sum of two of them is not -inf."""
+    g = torch.Generator().manual_seed(E)
+    lg = torch.randn(9, E, generator=g).cuda()
+    lg[3, ::2] = -float("inf")
+    lg[4] = -float("inf")
+    gs = E // G
+    for fill in (LOW, LOW / 1.5, -1.0e38, 2.5e38, torch.finfo(torch.float32).max):
+        b = torch.full((E,), fill)
+        spread = b.clone()
+        spread[gs:2 * gs] *= 0.75
+        some = b.clone()
+        some[[0, gs, E - 1]] = 0.25
+        one = b.clone()
+        one[gs:2 * gs] = 0.0
+        for bias in (b, spread, some, one):
+            bias = bias.cuda()
+            idx, w = select(lg, bias, k, score=score, n_groups=G, topk_groups=keep, group_value=value)
+            r_idx, r_w = gate(lg, bias, k, score=score, groups=G, keep=keep, value=value, scale=1.0)
+            np.testing.assert_array_equal(idx.cpu().numpy(), r_idx)
+            # roundings of float32 weights: twice an exponential (4, and the argument, up to 8 wide), a sum over 1024
+            # experts (37 deep) and one over 32, the quotient and the scale
+            np.testing.assert_allclose(w.cpu().numpy().astype(np.float64), r_w, rtol=(2 * (8 + 4) + 37 + 32 + 3) * 2.0 ** -24)
