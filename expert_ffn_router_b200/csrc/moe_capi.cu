@@ -210,6 +210,7 @@ static Dims layout_dims(const moe_config* c, size_t ws_bytes) {
 
 static moe_status check_ws(const moe_config* c, int T, void* ws, size_t ws_bytes) {
     MOE_TRY(check_ptr(ws, "ws"));
+    if (T > kWsMaxTokens) return fail(MOE_EINVAL, "a workspace holds at most 2^20 tokens");
     Dims l = dims_of(c, std::max(1, T), c->top_k + c->has_shared);
     const size_t need = ws_carve(l, nullptr).bytes;
     if (ws_bytes < need)
@@ -314,6 +315,10 @@ extern "C" {
 
 size_t moe_workspace_bytes(const moe_config* cfg, int32_t max_tokens) {
     if (check_cfg(cfg) != MOE_OK || max_tokens < 0) return 0;
+    if (max_tokens > kWsMaxTokens) {
+        fail(MOE_EINVAL, "a workspace holds at most 2^20 tokens");
+        return 0;
+    }
     const int S = cfg->top_k + cfg->has_shared;
     return ws_carve(dims_of(cfg, std::max(1, (int)max_tokens), S), nullptr).bytes;
 }

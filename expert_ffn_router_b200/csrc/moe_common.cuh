@@ -135,10 +135,12 @@ inline Ws ws_carve(const Dims& m, void* base) {
     return w;
 }
 
-// Largest T whose layout fits in `bytes` (0 if none): the layout of a
-// workspace is carved for this capacity, with S = top_k + has_shared slots.
+// Largest T whose layout fits in `bytes` (0 if none, at most kWsMaxTokens): the
+// layout of a workspace is carved for this capacity, with S = top_k +
+// has_shared slots.
+constexpr int kWsMaxTokens = 1 << 20;
 inline int ws_capacity(Dims m, size_t bytes) {
-    int lo = 0, hi = 1 << 20;
+    int lo = 0, hi = kWsMaxTokens;
     while (lo < hi) {
         const int mid = lo + (hi - lo + 1) / 2;
         m.T = mid;

@@ -122,7 +122,8 @@ typedef struct {
     int32_t n_slots;
 } moe_pool;
 
-/* Bytes of workspace the calls below need for up to max_tokens tokens. */
+/* Bytes of workspace the calls below need for up to max_tokens tokens, at most
+ * 2^20 (0 beyond; a call of more tokens on a workspace is MOE_EINVAL). */
 MOE_API size_t moe_workspace_bytes(const moe_config* cfg, int32_t max_tokens);
 
 /* Zero the whole workspace (its control words and counters).  Call once after
