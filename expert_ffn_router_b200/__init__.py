@@ -443,9 +443,14 @@ def moe_adapter_plan(n_adapters: int, adapter_of: torch.Tensor, plan: torch.Tens
 
 
 def adapter_plan(n_adapters: int, adapter_of: torch.Tensor, stream=None) -> torch.Tensor:
-    """Allocate (through torch) and make the plan of a batch."""
+    """Allocate (through torch) and make the plan of a batch.  It is the current
+    stream's memory: another ``stream`` that fills it waits for the current one
+    first, and calls that read it on a third wait for ``stream``."""
     plan = torch.empty(moe_adapter_plan_bytes(n_adapters, adapter_of.numel()), dtype=torch.uint8,
                        device=adapter_of.device)
+    if stream is not None and stream != torch.cuda.current_stream():
+        stream.wait_stream(torch.cuda.current_stream())  # the memory may be a plan's that is still read there
+        plan.record_stream(stream)
     moe_adapter_plan(n_adapters, adapter_of, plan, stream)
     return plan
 
