@@ -63,6 +63,7 @@ class MoeLayerOpts(ctypes.Structure):
 class MoePool(ctypes.Structure):
     _fields_ = [("w", ctypes.c_void_p), ("s", ctypes.c_void_p), ("slot_of", ctypes.c_void_p),
                 ("n_slots", ctypes.c_int32)]
+    _tensors = ()  # make_pool's
 
 
 class MoeCache(ctypes.Structure):
@@ -83,6 +84,7 @@ class MoeAdapters(ctypes.Structure):
     _fields_ = [("n_adapters", ctypes.c_int32), ("r_max", ctypes.c_int32), ("d_in", ctypes.c_int32),
                 ("d_out", ctypes.c_int32), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p),
                 ("rank", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+    _device = None  # make_adapters': the tables' device
 
 
 def config(d: int, f: int, n_experts: int, top_k: int, has_shared: int = 1, wbits: int = 4,
@@ -388,34 +390,37 @@ def moe_route_gated(cfg: MoeConfig, rule: MoeGateRule, x: torch.Tensor, w_router
                     bias: Optional[torch.Tensor], topk_idx: torch.Tensor, topk_w: torch.Tensor, ws: torch.Tensor,
                     stream=None):
     """moe_route with the selection of moe_gate."""
-    _here(x, "x")
-    T = x.shape[0]
+    dev = _here(x, "x")
+    T, n = x.shape[0], ws.numel()
     _check(lib.moe_route_gated(ctypes.byref(cfg), ctypes.byref(rule), _ptr(x, None, T * cfg.d, "x"), _xdtype(x), T,
-                               _ptr(w_router, torch.float32, cfg.n_experts * cfg.d, "w_router"),
-                               _ptr(bias, torch.float32, cfg.n_experts, "bias"),
-                               _ptr(topk_idx, torch.int32, T * cfg.top_k, "topk_idx"),
-                               _ptr(topk_w, torch.float32, T * cfg.top_k, "topk_w"),
-                               _ptr(ws, torch.uint8, name="ws"), ws.numel(), _stream(stream)), "moe_route_gated")
+                               _arg(w_router, dev, torch.float32, cfg.n_experts * cfg.d, "w_router"),
+                               None if bias is None else _arg(bias, dev, torch.float32, cfg.n_experts, "bias"),
+                               _arg(topk_idx, dev, torch.int32, T * cfg.top_k, "topk_idx"),
+                               _arg(topk_w, dev, torch.float32, T * cfg.top_k, "topk_w"),
+                               _arg(ws, dev, torch.uint8, n, "ws"), n, _stream(stream)), "moe_route_gated")
 
 
 def moe_layer_routed(cfg: MoeConfig, pool: MoePool, topk_idx: torch.Tensor, topk_w: torch.Tensor, x: torch.Tensor,
                      out: torch.Tensor, ws: torch.Tensor, accumulate: bool = False, stream=None):
     """moe_layer for a routing the caller has."""
-    _here(x, "x")
-    T = x.shape[0]
+    dev = _here(x, "x")
+    T, n = x.shape[0], ws.numel()
+    for t, name in zip(pool._tensors, ("pool.w", "pool.s", "pool.slot_of")):
+        if t is not None:
+            _here(t, name)
     _check(lib.moe_layer_routed(ctypes.byref(cfg), ctypes.byref(pool),
-                                _ptr(topk_idx, torch.int32, T * cfg.top_k, "topk_idx"),
-                                _ptr(topk_w, torch.float32, T * cfg.top_k, "topk_w"),
+                                _arg(topk_idx, dev, torch.int32, T * cfg.top_k, "topk_idx"),
+                                _arg(topk_w, dev, torch.float32, T * cfg.top_k, "topk_w"),
                                 _ptr(x, None, T * cfg.d, "x"), _xdtype(x), T,
-                                _ptr(out, torch.float32, T * cfg.d, "out"), 1 if accumulate else 0,
-                                _ptr(ws, torch.uint8, name="ws"), ws.numel(), _stream(stream)), "moe_layer_routed")
+                                _arg(out, dev, torch.float32, T * cfg.d, "out"), 1 if accumulate else 0,
+                                _arg(ws, dev, torch.uint8, n, "ws"), n, _stream(stream)), "moe_layer_routed")
 
 
 def make_adapters(a: torch.Tensor, b: torch.Tensor, rank: Optional[torch.Tensor] = None,
                   scale: Optional[torch.Tensor] = None) -> MoeAdapters:
     """The C struct over ``a`` [n][r_max][d_in] and ``b`` [n][d_out][r_max]
-    (bfloat16), ``rank`` [n] (int32) and ``scale`` [n] (float32); it keeps
-    references to them."""
+    (bfloat16), ``rank`` [n] (int32) and ``scale`` [n] (float32), all on one
+    device; it keeps references to them."""
     if a.dim() != 3 or b.dim() != 3 or a.shape[0] != b.shape[0] or a.shape[1] != b.shape[2]:
         raise ValueError(f"adapters: expected a [n][r][d_in] and b [n][d_out][r], got {list(a.shape)}, {list(b.shape)}")
     n, r, d_in = a.shape
@@ -423,6 +428,10 @@ def make_adapters(a: torch.Tensor, b: torch.Tensor, rank: Optional[torch.Tensor]
                      _ptr(b, torch.bfloat16, name="adapters.b"), _ptr(rank, torch.int32, n, "adapters.rank"),
                      _ptr(scale, torch.float32, n, "adapters.scale"))
     ad._tensors = (a, b, rank, scale)
+    ad._device = a.get_device()
+    for t, name in ((b, "b"), (rank, "rank"), (scale, "scale")):
+        if t is not None and t.get_device() != ad._device:
+            raise ValueError(f"adapters.{name}: expected a tensor on the device of adapters.a, {a.device}, got {t.device}")
     return ad
 
 
@@ -436,9 +445,9 @@ def moe_adapter_plan_bytes(n_adapters: int, max_tokens: int) -> int:
 def moe_adapter_plan(n_adapters: int, adapter_of: torch.Tensor, plan: torch.Tensor, stream=None):
     """The plan of a batch whose row t has the adapter ``adapter_of[t]`` (int32,
     -1: none), into ``plan``."""
-    _here(adapter_of, "adapter_of")
-    _check(lib.moe_adapter_plan(n_adapters, _ptr(adapter_of, torch.int32, name="adapter_of"), adapter_of.numel(),
-                                _ptr(plan, torch.uint8, name="plan"), plan.numel(), _stream(stream)),
+    dev, T, n = _here(adapter_of, "adapter_of"), adapter_of.numel(), plan.numel()
+    _check(lib.moe_adapter_plan(n_adapters, _arg(adapter_of, dev, torch.int32, T, "adapter_of"), T,
+                                _arg(plan, dev, torch.uint8, n, "plan"), n, _stream(stream)),
            "moe_adapter_plan")
 
 
@@ -460,6 +469,8 @@ def moe_adapter(ad: MoeAdapters, plan: torch.Tensor, x: torch.Tensor, y: torch.T
     """y = base + the rows' adapters of x (float32, bfloat16, or int8 codes
     with ``sx``); ``base`` may be ``y``; rows may lie apart."""
     dev = _here(x, "x")
+    if ad._device != dev and ad._device is not None:
+        raise ValueError(f"adapters: expected tables on the current device, cuda:{dev}, got cuda:{ad._device}")
     T = x.shape[0]
     xp, ldx = _rows(x, dev, ad.d_in, "x")
     yp, ldy = _rows(y, dev, ad.d_out, "y", torch.float32)
