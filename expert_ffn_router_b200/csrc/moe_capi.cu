@@ -12,6 +12,7 @@
 
 #include "moe.h"
 #include "moe_launch.h"
+#include "moe_optin.h"
 #include "moe_decode.cuh"
 #include "moe_route.cuh"
 
@@ -33,7 +34,7 @@ static moe_status cuda_fail(cudaError_t e, const char* where) {
 // ---------------------------------------------------------------------------
 static std::mutex g_mu;
 static std::unordered_map<unsigned long long, int> g_grid;  // (device, func, smem) -> grid
-static std::unordered_map<unsigned long long, size_t> g_smem;
+static OptIn g_smem;  // (device, func) -> dynamic shared memory
 
 static unsigned long long cache_key(int dev, const void* func, size_t smem) {
     return ((unsigned long long)(uintptr_t)func * 1000003ull) ^ ((unsigned long long)smem << 20) ^
@@ -71,18 +72,9 @@ cudaError_t allow_smem(const void* func, size_t smem) {
     if (smem + 4096 <= 48 * 1024) return cudaSuccess;
     int dev = 0;
     cudaGetDevice(&dev);
-    const unsigned long long key = cache_key(dev, func, 0);
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        auto it = g_smem.find(key);
-        if (it != g_smem.end() && it->second >= smem) return cudaSuccess;
-    }
-    cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) {
-        std::lock_guard<std::mutex> lk(g_mu);
-        g_smem[key] = smem;
-    }
-    return e;
+    return g_smem.raise(cache_key(dev, func, 0), smem, [&](size_t n) {
+        return cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)n);
+    });
 }
 
 static int round_ncl(int ncl, bool down) {
