@@ -102,6 +102,17 @@ ExpertTiling expert_tiling(int d, int f, int wb) {
 // ---------------------------------------------------------------------------
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
+// The fields that the selection of experts uses.
+moe_status check_selection(const moe_config* c) {
+    if (!c) return fail(MOE_EINVAL, "cfg is NULL");
+    if (c->n_experts < 1 || c->n_experts > 1024) return fail(MOE_EINVAL, "n_experts must be in [1, 1024]");
+    if (c->top_k < 1 || c->top_k > 32 || c->top_k > c->n_experts)
+        return fail(MOE_EINVAL, "top_k must be in [1, min(n_experts, 32)]");
+    if (!(c->routed_scale == c->routed_scale)) return fail(MOE_EINVAL, "routed_scale is NaN");
+    if (!(c->topp >= 0.0f && c->topp <= 1.0f)) return fail(MOE_EINVAL, "topp must be in [0, 1]");
+    return MOE_OK;
+}
+
 moe_status check_cfg(const moe_config* c) {
     if (!c) return fail(MOE_EINVAL, "cfg is NULL");
     if (c->d <= 0 || c->f <= 0 || c->d > 8192 || c->f > 8192)
@@ -109,13 +120,8 @@ moe_status check_cfg(const moe_config* c) {
     if (c->wbits != 4 && c->wbits != 2 && c->wbits != 8) return fail(MOE_EINVAL, "wbits must be 4, 2 or 8");
     if ((c->d * c->wbits / 8) % 16 || (c->f * c->wbits / 8) % 16 || (c->d * c->wbits) % 8 || (c->f * c->wbits) % 8)
         return fail(MOE_EINVAL, "d*wbits/8 and f*wbits/8 must be multiples of 16 bytes");
-    if (c->n_experts < 1 || c->n_experts > 1024) return fail(MOE_EINVAL, "n_experts must be in [1, 1024]");
-    if (c->top_k < 1 || c->top_k > 32 || c->top_k > c->n_experts)
-        return fail(MOE_EINVAL, "top_k must be in [1, min(n_experts, 32)]");
     if (c->has_shared != 0 && c->has_shared != 1) return fail(MOE_EINVAL, "has_shared must be 0 or 1");
-    if (!(c->routed_scale == c->routed_scale)) return fail(MOE_EINVAL, "routed_scale is NaN");
-    if (!(c->topp >= 0.0f && c->topp <= 1.0f)) return fail(MOE_EINVAL, "topp must be in [0, 1]");
-    return MOE_OK;
+    return check_selection(c);
 }
 
 // A cached pool (slot_of set) holds n_slots >= 1 blobs; its table is device memory.

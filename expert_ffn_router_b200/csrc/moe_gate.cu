@@ -95,7 +95,7 @@ using namespace moe;
 extern "C" moe_status moe_gate(const moe_config* cfg, const moe_gate_rule* rule, const void* logits, moe_dtype dtype,
                                int64_t ld, int32_t T, const float* bias, int32_t* topk_idx, float* topk_w,
                                moe_stream_t stream) try {
-    moe_status st = check_cfg(cfg);
+    moe_status st = check_selection(cfg);
     if (st != MOE_OK) return st;
     if ((st = check_rule(cfg, rule)) != MOE_OK) return st;
     if ((st = check_dtype(dtype)) != MOE_OK) return st;

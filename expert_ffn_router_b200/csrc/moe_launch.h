@@ -43,6 +43,7 @@ cudaError_t launch_down(const Params& p, const ExpertTiling& tl, bool dbg, cudaS
 
 // Expert selection from logits (moe_gate.cu): logits [nplanes][T][E] with rows
 // ld and planes `plane` elements apart.
+moe_status check_selection(const moe_config* c);
 moe_status check_rule(const moe_config* c, const moe_gate_rule* r);
 cudaError_t launch_gate(const moe_config* c, const moe_gate_rule* r, const void* logits, moe_dtype dt, long long ld,
                         int nplanes, long long plane, int T, const float* bias, int32_t* idx, float* w,

@@ -299,7 +299,7 @@ MOE_API moe_status moe_rmsnorm(const void* x, moe_dtype dtype, int32_t T, int32_
  * Limits (MOE_EINVAL otherwise): n_groups <= 32, a divisor of n_experts;
  * 1 <= topk_groups <= n_groups; top_k <= topk_groups * n_experts / n_groups.
  * n_groups 0 or 1: no groups, topk_groups and group_value are not read.  Of
- * cfg only n_experts, top_k, routed_scale and topp are used.
+ * cfg moe_gate uses (and checks) only n_experts, top_k, routed_scale and topp.
  * ------------------------------------------------------------------------- */
 enum { MOE_SCORE_SIGMOID = 0, MOE_SCORE_SOFTMAX = 1 };
 enum { MOE_GROUP_TOP2 = 0, MOE_GROUP_MAX = 1 };
