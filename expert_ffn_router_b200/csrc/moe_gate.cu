@@ -59,7 +59,8 @@ static cudaError_t launch_gate_v(const GateArgs& a, cudaStream_t s) {
 template <typename LT>
 static cudaError_t launch_gate_l(const GateArgs& a, cudaStream_t s) {
     // four neighbours at a time where every row (and plane) starts on them
-    const bool vec = a.E > 64 && a.E % 4 == 0 && a.ld % 4 == 0 && a.plane % 4 == 0;
+    const bool vec = a.E > 64 && a.E % 4 == 0 && a.ld % 4 == 0 && a.plane % 4 == 0 &&
+                     (uintptr_t)a.logits % (4 * sizeof(LT)) == 0;
     return vec ? launch_gate_v<LT, true>(a, s) : launch_gate_v<LT, false>(a, s);
 }
 
@@ -102,7 +103,8 @@ extern "C" moe_status moe_gate(const moe_config* cfg, const moe_gate_rule* rule,
     if (T < 0) return fail(MOE_EINVAL, "T < 0");
     if (ld < cfg->n_experts) return fail(MOE_EINVAL, "ld is smaller than n_experts");
     if (T == 0) return MOE_OK;
-    if ((st = check_ptr(logits, "logits")) != MOE_OK) return st;
+    if (!logits) return fail(MOE_EINVAL, "logits is NULL");
+    if ((uintptr_t)logits % (dtype == MOE_BF16 ? 2 : 4)) return fail(MOE_EALIGN, "logits is not aligned to its elements");
     if ((st = check_ptr(bias, "bias", true)) != MOE_OK) return st;
     if ((st = check_ptr(topk_idx, "topk_idx")) != MOE_OK) return st;
     if ((st = check_ptr(topk_w, "topk_w")) != MOE_OK) return st;

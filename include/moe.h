@@ -15,7 +15,8 @@
  * Conventions for every call:
  *  - Tensor pointers are DEVICE pointers owned by the caller.  The library
  *    never allocates, frees or keeps caller memory beyond the stream work it
- *    enqueues.  Pointers must be 16-byte aligned (MOE_EALIGN otherwise).
+ *    enqueues.  Pointers must be 16-byte aligned (MOE_EALIGN otherwise;
+ *    moe_gate's logits: aligned to their elements).
  *  - All work is enqueued on `stream` (a cudaStream_t; NULL = legacy default
  *    stream) with no implicit synchronisation.  Argument errors are detected
  *    on the host before anything is enqueued and return synchronously.  A
@@ -311,9 +312,11 @@ typedef struct {
     int32_t raw_weights; /* 1: weights are not renormalised */
 } moe_gate_rule;
 
-/* logits [T][E] (MOE_F32 or MOE_BF16), rows ld >= E elements apart; bias fp32
- * [E] or NULL -> topk_idx int32 [T][top_k], topk_w fp32 [T][top_k], as
- * moe_route writes them.  No workspace. */
+/* logits [T][E] (MOE_F32 or MOE_BF16), rows ld >= E elements apart, from any
+ * element on: the pointer need not be 16-byte aligned (rows that start on four
+ * elements, with E a multiple of 4, are read four at a time); bias fp32 [E] or
+ * NULL -> topk_idx int32 [T][top_k], topk_w fp32 [T][top_k], as moe_route
+ * writes them.  The outputs overlap none of the inputs.  No workspace. */
 MOE_API moe_status moe_gate(const moe_config* cfg, const moe_gate_rule* rule, const void* logits, moe_dtype dtype,
                             int64_t ld, int32_t T, const float* bias, int32_t* topk_idx, float* topk_w,
                             moe_stream_t stream);
