@@ -41,3 +41,32 @@ def test_logits_off_their_own_size_are_refused():
         st = M.lib.moe_gate(ctypes.byref(c), ctypes.byref(r), at + off, dtype, 8, 3, None, idx.data_ptr(), w.data_ptr(),
                             torch.cuda.current_stream().cuda_stream)
         assert st == want
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_beyond_32_bits(dtype):
+    """The last row starts 2^32 elements behind the first."""
+    E, k, ld = 64, 6, 1 << 31
+    wide = torch.empty(2 * ld + E, dtype=dtype, device="cuda")
+    lg = torch.as_strided(wide, (3, E), (ld, 1))
+    lg.copy_(torch.randn(3, E, generator=torch.Generator().manual_seed(3)).to(dtype))
+    idx = torch.empty(3, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(3, k, device="cuda")
+    M.moe_gate(M.config(128, 64, E, k), M.gate_rule("sigmoid", 8, 4), lg, None, idx, w)
+    r_idx, _ = gate(lg, None, k, groups=8, keep=4)
+    np.testing.assert_array_equal(idx.cpu().numpy(), r_idx)
+
+
+def test_many_rows():
+    """More outputs than 2^31 bytes, more rows than any grid."""
+    T, E, k = (1 << 24) + 5, 40, 32
+    lg = torch.randint(-20, 20, (T, E), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").bfloat16()
+    lg[:, ::5] = -float("inf")
+    idx = torch.full((T + 1, k), -7, dtype=torch.int32, device="cuda")
+    w = torch.full((T + 1, k), -7.0, device="cuda")
+    M.moe_gate(M.config(128, 64, E, k, routed_scale=1.0), M.gate_rule("softmax"), lg, None, idx[:T], w[:T])
+    key = lg.to(torch.int32).masked_fill(lg == -float("inf"), -100) * 64 + (63 - torch.arange(E, device="cuda")).int()
+    want = torch.sort(key, dim=1, descending=True)[1][:, :k].to(torch.int32)
+    assert torch.equal(idx[:T], want)  # 32 of 40 can be selected
+    assert (w[:T].sum(1) - 1).abs().max() < 40 * 2.0 ** -24
+    assert (idx[T] == -7).all() and (w[T] == -7.0).all()
