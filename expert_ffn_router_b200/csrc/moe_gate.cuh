@@ -153,7 +153,7 @@ static __device__ __noinline__ void gate_row_f64(const GateArgs& a, int t, doubl
     const double sum = warp_sum_f64(s);
     if (lane < k) {
         a.idx[(size_t)t * k + lane] = my_e;
-        a.w[(size_t)t * k + lane] = (float)((a.raw ? s : sum > 0.0 ? s / sum : 0.0) * (double)a.scale);
+        a.w[(size_t)t * k + lane] = my_e < 0 ? 0.0f : (float)((a.raw ? s : sum > 0.0 ? s / sum : 0.0) * (double)a.scale);
     }
 }
 

@@ -96,3 +96,15 @@ def test_groups_whose_sums_leave_float32(score, value, E, G, keep, k):
             # roundings of float32 weights: twice an exponential (4, and the argument, up to 8 wide), a sum over 1024
             # experts (37 deep) and one over 32, the quotient and the scale
             np.testing.assert_allclose(w.cpu().numpy().astype(np.float64), r_w, rtol=(2 * (8 + 4) + 37 + 32 + 3) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+def test_slots_without_an_expert_weigh_nothing_whatever_the_scale(renorm):
+    """An infinite routed_scale too; rows of both forms (the second one's
+    infinite logit sends it through the double-precision one)."""
+    lg = torch.full((3, 64), -float("inf"), device="cuda")
+    lg[0, 3] = 1.0
+    lg[1, 3], lg[1, 9] = float("inf"), 2.0
+    idx, w = select(lg, None, 6, scale=float("inf"), score="sigmoid", renorm=renorm)
+    assert idx.tolist() == [[3] + [-1] * 5, [3, 9] + [-1] * 4, [-1] * 6]
+    assert (w[idx < 0] == 0).all() and (w[idx >= 0] == float("inf")).all()
