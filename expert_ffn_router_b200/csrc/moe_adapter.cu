@@ -18,11 +18,20 @@
 namespace moe {
 
 // Which of the two kernels takes a call.  k_adapter (tasks of 64 rows on
-// tcgen05) needs long tasks and ranks that keep mma.sync busy; measured at
-// d = 6144, bf16 rows in runs, us with k_adapter_few and with k_adapter: rank 64,
-// 16 adapters, 2900 rows 97 and 64, 8192 rows 210 and 118; rank 16, 8192 rows 119
-// and 111, in fp32 144 and 204; rank 64, 64 adapters, rows mixed, 8192 rows 228
-// and 369.
+// tcgen05) needs long tasks and ranks that keep mma.sync busy.  Measured (B200,
+// d = 6144, rank 64, base given; us with k_adapter_few and with k_adapter, rows
+// in runs | mixed):
+//   8192 rows of 16 adapters   bf16 214 126 | 215 211   fp32 265 204 | 265 205   codes 220 153 | 220 152
+//   8192 rows of 64 adapters   bf16 240 176 | 240 280   fp32 295 293 | 295 295   codes 247 214 | 248 212
+//   2048 rows of 4 adapters    bf16  69  59 |  69 105   fp32  84 100 |  84 100   codes  71  74 |  71  74
+//   2048 rows of 16 adapters   bf16  70  63 |  70 106   fp32  84 101 |  84 101   codes  71  80 |  71  78
+// rank 128, 8 adapters in runs, 8192 rows: bf16 437 143, fp32 525 213; 2048 rows:
+// bf16 129 74, fp32 154 108.  Rank 16, bf16 in runs, 8192 rows: 119 111, fp32 144
+// 204.  The host knows the adapters of the table, not those that the batch uses,
+// nor whether its rows lie in runs (the plan does, on the device), so the rule
+// does not take the faster kernel everywhere: 8192 rows of 16 adapters of a table
+// of more than 32 (and of 64 adapters, in runs) run on k_adapter_few, 2048 mixed
+// bf16 rows and 2048 fp32 rows of up to 8 adapters on k_adapter.
 static bool ad_few(const AdArgs& g) {
     return g.r_max <= 32 || g.T < 2048 || g.T / 256 < g.n;
 }

@@ -318,15 +318,12 @@ __device__ __forceinline__ void ad_copy_row(const float* base, float* y, int w) 
 // tiled copies, which keep a ring of stages full through both products and on
 // into the next task; NP put rows that are not bf16 into their parts, and clear
 // what lies in B behind a rank that is no multiple of 16.
-// Measured (B200, 8192 bf16 rows of 6144, 16 adapters, ranks 4 to 64): 117 us,
-// 4.4 TB/s of the rows, base and outputs, 0.67 of a copy; product 1 takes 24 us of
-// a CTA's time, the meeting 4, product 2 78 -- the rows of base and y, which every
-// SM moves at the same time.  On the way there: 195 us with mma.sync and every
-// lane copying 16 bytes at a time; 160 with warps of their own for that; 240 with
-// tcgen05 fed by them, because a lane's address arithmetic set the pace; 460 with a
-// bulk copy for each row's few hundred bytes (80 cycles of the copy engine each);
-// 266 with tiled copies, but a gather of four rows for each four rows of x (now
-// only where rows do not lie together) and 8 adding warps; 137 with 16 of them.
+// Measured (B200, 8192 bf16 rows of 6144 in runs, 16 adapters, ranks 4 to 64): 117
+// us, 4.4 TB/s of the rows, base and outputs, 0.67 of a copy.  The adding warps
+// drain product 1, meet and drain product 2 in turn, so base and y do not move
+// meanwhile.  Rows that do not lie together are gathered four at a time: rank 64
+// throughout, 126 us in runs, 211 mixed; float32 rows, which pass the parting
+// warps either way, 204 and 205.
 // RT: components held, a multiple of 16, at least r_max.
 // ---------------------------------------------------------------------------
 template <typename XT, int RT>
@@ -352,7 +349,9 @@ struct AdTile {
     static constexpr int SMEM = NS * STAGE + REST + 1024;
     // D1 is read out and begun anew every FLUSH stages (32 to 48 steps of the
     // MMA), the parts added in registers: a sum over all 6144 columns within
-    // tensor memory was off by 2.8e-6 of the result (its adder truncates).
+    // tensor memory was off by 2.8e-6 of the result (its adder truncates); so y is
+    // off by 5e-7 for bf16 rows and 1.1e-6 for float32 ones, whose three parts are 48
+    // steps (rank 64, no base; plain float32 products: 3e-7 and 6e-7).
     static constexpr int FLUSH = KB >= 4 ? 2 : KB == 3 ? 3 : 4;
     // tensor memory: D2 2 x 2 x NR columns, D1 2 x NR.  No CTA of a kernel that
     // uses tensor memory fits beside this one, so its columns are free.

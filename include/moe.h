@@ -274,8 +274,10 @@ MOE_API moe_status moe_rmsnorm(const void* x, moe_dtype dtype, int32_t T, int32_
  *
  * moe_route computes one rule (sigmoid scores plus bias, any expert, weights
  * renormalised) on logits that it keeps to itself.  moe_gate takes the logits
- * of any router and selects by a moe_gate_rule; a zero-initialised rule is
- * moe_route's.  For a row l[0..E) of logits and a bias b[0..E) (NULL: none):
+ * of any router and selects by a moe_gate_rule; a zero-initialised rule states
+ * moe_route's (which compares values, and sums for the truncation, in float32:
+ * where two are nearer than float32 tells apart the two calls may differ).
+ * For a row l[0..E) of logits and a bias b[0..E) (NULL: none):
  *  - an expert can be selected unless its logit or its bias is NaN or -inf
  *    (a caller masks experts by logits of -inf);
  *  - score s_e = 1 / (1 + exp(-l_e)) (MOE_SCORE_SIGMOID), or
@@ -297,6 +299,9 @@ MOE_API moe_status moe_rmsnorm(const void* x, moe_dtype dtype, int32_t T, int32_
  * Scores, group values, selection values and the truncation's sums are
  * compared as double precision gives them, so near-equal experts take the
  * same order on every path of the kernel; logits of one value tie exactly.
+ * Weights are float32 throughout (within a few roundings).  Mask by -inf: finite
+ * mask values select rightly, but without a bias values far below the other
+ * logits (-1e9, the type's lowest) make a row up to 7 times slower.
  * Limits (MOE_EINVAL otherwise): n_groups <= 32, a divisor of n_experts;
  * 1 <= topk_groups <= n_groups; top_k <= topk_groups * n_experts / n_groups.
  * n_groups 0 or 1: no groups, topk_groups and group_value are not read.  Of
